@@ -20,7 +20,7 @@ __all__ = [
     "grouped_fp8_gemm", "fp4_gemm", "grouped_fp4_gemm", "quantize_fp8_1x128",
     "quantize_nvfp4", "grouped_fp8_gemm_tune", "fp4_gemm_tune", "grouped_fp4_gemm_tune",
     "tuned_tile", "tune_clear", "fp4_gemm_problems", "fp8_gemm_problems", "grouped_w4a16_gemm",
-    "rank_tiles",
+    "rank_tiles", "rope_kv_append", "paged_decode_attention", "prompt_attention",
     "num_tiles",
     "device_info", "library_path", "load_library", "FP8", "FP4",
 ]
@@ -71,6 +71,16 @@ class _Fp8Problem(ctypes.Structure):
 class _Options(ctypes.Structure):
     _fields_ = [("tile_id", ctypes.c_int), ("max_workgroups", ctypes.c_int),
                 ("run_split", ctypes.c_int), ("run_align", ctypes.c_int)]
+
+
+def __getattr__(name):
+    # the attention entry points live in a module that imports torch, which
+    # the C-ABI checks do without
+    if name in ("rope_kv_append", "paged_decode_attention", "prompt_attention"):
+        from . import attention
+        globals()[name] = getattr(attention, name)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def load_library():

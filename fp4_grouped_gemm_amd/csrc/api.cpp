@@ -23,6 +23,7 @@
 #include <vector>
 
 #include "../../include/fgg.h"
+#include "attn.h"
 #include "common.h"
 
 namespace {
@@ -741,6 +742,224 @@ fgg_status quantize_nvfp4_static_rows(const void* X, const int32_t* rows, void* 
                                                      static_cast<uint8_t*>(scale), global_scale, R,
                                                      K, d->num_cus,
                                                      static_cast<hipStream_t>(stream), rows, T));
+}
+
+// ---------------------------------------------------------------- attention
+// Head layout shared by the attention entry points.
+static fgg_status check_heads(const char* fn, int q_heads, int kv_heads, int head_dim) {
+  if (kv_heads < 1 || kv_heads > (1 << 10))
+    return fail(FGG_EINVAL, fn, "requires 1 <= kv_heads <= 2^10, got %d", kv_heads);
+  if (q_heads < kv_heads || q_heads > (1 << 12) || q_heads % kv_heads)
+    return fail(FGG_EINVAL, fn, "q_heads must be a multiple of kv_heads=%d and at most 2^12, got %d",
+                kv_heads, q_heads);
+  if (head_dim != 64 && head_dim != 128)
+    return fail(FGG_EUNSUPPORTED, fn, "head_dim %d is not supported: 64 or 128", head_dim);
+  return FGG_OK;
+}
+
+// Token and head strides (in values) of a BF16 operand read or written in
+// 16-byte pieces.
+static fgg_status check_rows16(const char* fn, const char* name, const void* p, long long token,
+                               long long head) {
+  if (!p) return fail(FGG_EINVAL, fn, "%s is null", name);
+  if (token < 0 || head < 0) return fail(FGG_EINVAL, fn, "%s has a negative stride", name);
+  if (!aligned(p, 16) || token % 8 || head % 8)
+    return fail(FGG_EALIGN, fn, "%s must be 16-byte aligned, its strides multiples of 8 values", name);
+  return FGG_OK;
+}
+
+static fgg_status check_cache(const char* fn, const fgg_kv_cache* c, fgg::KvCache* out) {
+  if (!c) return fail(FGG_EINVAL, fn, "cache is null");
+  if (!c->k || !c->v || !c->page_table)
+    return fail(FGG_EINVAL, fn, "null pointer among k, v, page_table of the cache");
+  if (c->dtype != FGG_KV_BF16 && c->dtype != FGG_KV_E4M3)
+    return fail(FGG_EINVAL, fn, "bad cache dtype %d", c->dtype);
+  if (c->num_pages < 1) return fail(FGG_EINVAL, fn, "requires num_pages >= 1, got %d", c->num_pages);
+  if (c->page_size < 1 || c->page_size > (1 << 16))
+    return fail(FGG_EINVAL, fn, "requires 1 <= page_size <= 2^16, got %d", c->page_size);
+  if (c->page_size & (c->page_size - 1))
+    return fail(FGG_EUNSUPPORTED, fn, "page_size %d is not supported: powers of two only", c->page_size);
+  if (c->batch < 1 || c->batch > (1 << 20))
+    return fail(FGG_EINVAL, fn, "requires 1 <= batch <= 2^20, got %d", c->batch);
+  if (c->table_width < 1) return fail(FGG_EINVAL, fn, "requires table_width >= 1, got %d", c->table_width);
+  if ((long long)c->table_width * c->page_size > 0x7FFFFFFFLL)
+    return fail(FGG_EUNSUPPORTED, fn, "table_width * page_size must stay below 2^31 tokens");
+  if (c->table_stride < 0) return fail(FGG_EINVAL, fn, "page_table has a negative stride");
+  const bool fp8 = c->dtype == FGG_KV_E4M3;
+  if (!fp8 && (c->k_scale || c->v_scale))
+    return fail(FGG_EINVAL, fn, "k_scale and v_scale go with an E4M3 cache");
+  const int bytes = fp8 ? 1 : 2;
+  for (int i = 0; i < 3; ++i) {
+    if (c->k_strides[i] < 0 || c->v_strides[i] < 0)
+      return fail(FGG_EINVAL, fn, "the cache has a negative stride");
+    if (c->k_strides[i] * bytes % 16 || c->v_strides[i] * bytes % 16)
+      return fail(FGG_EALIGN, fn, "the strides of the cache must be multiples of 16 bytes");
+  }
+  if (!aligned(c->k, 16) || !aligned(c->v, 16))
+    return fail(FGG_EALIGN, fn, "k and v of the cache must be 16-byte aligned");
+  if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) || !aligned(c->page_table, 4))
+    return fail(FGG_EALIGN, fn, "page_table, k_scale and v_scale must be 4-byte aligned");
+  out->k = static_cast<uint8_t*>(c->k);
+  out->v = static_cast<uint8_t*>(c->v);
+  out->k_page = c->k_strides[0] * bytes;
+  out->k_head = c->k_strides[1] * bytes;
+  out->k_token = c->k_strides[2] * bytes;
+  out->v_page = c->v_strides[0] * bytes;
+  out->v_head = c->v_strides[1] * bytes;
+  out->v_token = c->v_strides[2] * bytes;
+  out->k_scale = c->k_scale;
+  out->v_scale = c->v_scale;
+  out->table = c->page_table;
+  out->table_stride = c->table_stride;
+  out->num_pages = c->num_pages;
+  out->kv_heads = c->kv_heads;
+  out->page_shift = __builtin_ctz((unsigned)c->page_size);
+  out->batch = c->batch;
+  out->width = c->table_width;
+  out->fp8 = fp8;
+  return FGG_OK;
+}
+
+fgg_status rope_kv_append(const fgg_kv_cache* cache, const void* q, const void* k, const void* v,
+                          const long long* strides, const float* turns, int num_turns, int rot_dim,
+                          int interleaved, const int32_t* positions, const int32_t* seq_ids,
+                          void* q_out, void* k_out, int T, int q_heads, void* stream) {
+  const char* fn = "rope_kv_append";
+  fgg::AppendArgs a{};
+  fgg_status st = check_cache(fn, cache, &a.c);
+  if (st != FGG_OK) return st;
+  if ((st = check_heads(fn, q_heads, cache->kv_heads, cache->head_dim)) != FGG_OK) return st;
+  if (!strides) return fail(FGG_EINVAL, fn, "strides is null");
+  if ((st = check_rows16(fn, "q", q, strides[0], strides[1])) != FGG_OK) return st;
+  if ((st = check_rows16(fn, "k", k, strides[2], strides[3])) != FGG_OK) return st;
+  if ((st = check_rows16(fn, "v", v, strides[4], strides[5])) != FGG_OK) return st;
+  if (!turns || !positions || !q_out)
+    return fail(FGG_EINVAL, fn, "null pointer among cos_sin, positions, q_out");
+  if (T < 1 || T > (1 << 24)) return fail(FGG_EINVAL, fn, "requires 1 <= T <= 2^24, got T=%d", T);
+  if (num_turns < 1) return fail(FGG_EINVAL, fn, "cos_sin has no rows");
+  if (rot_dim < 2 || rot_dim > cache->head_dim || rot_dim % 2)
+    return fail(FGG_EINVAL, fn, "rot_dim must be even, at least 2 and at most head_dim=%d, got %d",
+                cache->head_dim, rot_dim);
+  if (rot_dim % 16) return fail(FGG_EUNSUPPORTED, fn, "rot_dim %% 16 != 0 (%d) is not supported", rot_dim);
+  if (!seq_ids && T != cache->batch)
+    return fail(FGG_EINVAL, fn, "without seq_ids there is one token a sequence: T=%d, batch=%d", T,
+                cache->batch);
+  if ((long long)T * (q_heads + 2 * cache->kv_heads) * (cache->head_dim / 16) > 0x7FFFFFFFLL)
+    return fail(FGG_EUNSUPPORTED, fn, "requires T * (q_heads + 2 kv_heads) * head_dim / 16 < 2^31");
+  if (!aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(turns, 16))
+    return fail(FGG_EALIGN, fn, "q_out, k_out and cos_sin must be 16-byte aligned");
+  if (!aligned(positions, 4) || !aligned(seq_ids, 4))
+    return fail(FGG_EALIGN, fn, "positions and seq_ids must be 4-byte aligned");
+  const DeviceFacts* d = current_device(fn, &st);
+  if (!d) return st;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_token = strides[0];
+  a.q_head = strides[1];
+  a.k_token = strides[2];
+  a.k_head = strides[3];
+  a.v_token = strides[4];
+  a.v_head = strides[5];
+  a.turns = turns;
+  a.positions = positions;
+  a.seq_ids = seq_ids;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_out = static_cast<uint16_t*>(k_out);
+  a.T = T;
+  a.q_heads = q_heads;
+  a.D = cache->head_dim;
+  a.rot = rot_dim;
+  a.npos = num_turns;
+  a.interleaved = interleaved != 0;
+  return launched(fn, fgg::launch_append(a, static_cast<hipStream_t>(stream)));
+}
+
+// Checks of a decode call that also size its workspace.
+static fgg_status decode_prepare(const char* fn, const fgg_kv_cache* cache, int q_heads,
+                                 fgg::DecodeArgs* a, int* workgroups) {
+  fgg_status st = check_cache(fn, cache, &a->c);
+  if (st != FGG_OK) return st;
+  if ((st = check_heads(fn, q_heads, cache->kv_heads, cache->head_dim)) != FGG_OK) return st;
+  const long long tokens = (long long)cache->table_width * cache->page_size;
+  if ((long long)cache->batch * q_heads * (tokens / 128 + 1) > (1LL << 30))
+    return fail(FGG_EUNSUPPORTED, fn, "requires batch * q_heads * table tokens / 128 <= 2^30");
+  const DeviceFacts* d = current_device(fn, &st);
+  if (!d) return st;
+  *workgroups = fgg::decode_workgroups(cache->batch, q_heads, cache->kv_heads, tokens, d->num_cus);
+  return FGG_OK;
+}
+
+fgg_status paged_decode_attention_workspace(const fgg_kv_cache* cache, int q_heads, size_t* bytes) {
+  const char* fn = "paged_decode_attention_workspace";
+  if (!bytes) return fail(FGG_EINVAL, fn, "bytes is null");
+  fgg::DecodeArgs a{};
+  int workgroups = 0;
+  fgg_status st = decode_prepare(fn, cache, q_heads, &a, &workgroups);
+  if (st != FGG_OK) return st;
+  *bytes = fgg::decode_workspace(workgroups, cache->head_dim);
+  g_err.clear();
+  return FGG_OK;
+}
+
+fgg_status paged_decode_attention(const fgg_kv_cache* cache, const void* q, long long q_seq_stride,
+                                  long long q_head_stride, const int32_t* lengths, float scale,
+                                  void* out, int q_heads, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  const char* fn = "paged_decode_attention";
+  fgg::DecodeArgs a{};
+  int workgroups = 0;
+  fgg_status st = check_rows16(fn, "q", q, q_seq_stride, q_head_stride);
+  if (st != FGG_OK) return st;
+  if (!lengths || !out || !workspace)
+    return fail(FGG_EINVAL, fn, "null pointer among lengths, out, workspace");
+  if (!std::isfinite(scale)) return fail(FGG_EINVAL, fn, "scale must be finite");
+  if (!aligned(out, 16) || !aligned(workspace, 16))
+    return fail(FGG_EALIGN, fn, "out and workspace must be 16-byte aligned");
+  if (!aligned(lengths, 4)) return fail(FGG_EALIGN, fn, "lengths must be 4-byte aligned");
+  if ((st = decode_prepare(fn, cache, q_heads, &a, &workgroups)) != FGG_OK) return st;
+  const size_t need = fgg::decode_workspace(workgroups, cache->head_dim);
+  if (workspace_bytes < need)
+    return fail(FGG_EINVAL, fn, "workspace of %zu bytes, needs %zu", workspace_bytes, need);
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_seq = q_seq_stride;
+  a.q_head = q_head_stride;
+  a.lengths = lengths;
+  a.out = static_cast<uint16_t*>(out);
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = a.part_o + (size_t)workgroups * 2 * 16 * cache->head_dim;
+  a.scale = scale;
+  a.q_heads = q_heads;
+  a.D = cache->head_dim;
+  return launched(fn, fgg::launch_decode(a, workgroups, static_cast<hipStream_t>(stream)));
+}
+
+fgg_status prompt_attention(const void* q, const void* k, const void* v, const long long* strides,
+                            const int32_t* starts, float scale, void* out, int T, int batch,
+                            int q_heads, int kv_heads, int head_dim, void* stream) {
+  const char* fn = "prompt_attention";
+  fgg_status st = check_heads(fn, q_heads, kv_heads, head_dim);
+  if (st != FGG_OK) return st;
+  if (!strides) return fail(FGG_EINVAL, fn, "strides is null");
+  if ((st = check_rows16(fn, "q", q, strides[0], strides[1])) != FGG_OK) return st;
+  if ((st = check_rows16(fn, "k", k, strides[2], strides[3])) != FGG_OK) return st;
+  if ((st = check_rows16(fn, "v", v, strides[4], strides[5])) != FGG_OK) return st;
+  if (!starts || !out) return fail(FGG_EINVAL, fn, "null pointer among starts, out");
+  if (!std::isfinite(scale)) return fail(FGG_EINVAL, fn, "scale must be finite");
+  if (T < 1 || T > (1 << 24)) return fail(FGG_EINVAL, fn, "requires 1 <= T <= 2^24, got T=%d", T);
+  if (batch < 1 || batch > (1 << 20))
+    return fail(FGG_EINVAL, fn, "requires 1 <= batch <= 2^20, got %d", batch);
+  if (!aligned(out, 16)) return fail(FGG_EALIGN, fn, "out must be 16-byte aligned");
+  if (!aligned(starts, 4)) return fail(FGG_EALIGN, fn, "starts must be 4-byte aligned");
+  if (((long long)T / 64 + batch + 2) * q_heads > 0x7FFFFFFFLL)
+    return fail(FGG_EUNSUPPORTED, fn, "requires (T / 64 + batch + 2) * q_heads < 2^31");
+  const DeviceFacts* d = current_device(fn, &st);
+  if (!d) return st;
+  const fgg::PromptArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
+                          static_cast<const uint16_t*>(v), strides[0], strides[1], strides[2],
+                          strides[3], strides[4], strides[5], starts, static_cast<uint16_t*>(out),
+                          scale, T, batch, q_heads, kv_heads, head_dim};
+  return launched(fn, fgg::launch_prompt(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,416 @@
+// paged_decode_attention: one new token a sequence against a paged cache.
+//
+//   o[h] = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q_h . k_t - m),
+//   m = max_t scale q_h . k_t  over the cached tokens t of the sequence.
+//
+// One pass over the cache with the running maximum and sum; every key and
+// value is read once for the (up to 16) query heads of its KV head, so the
+// kernel is bound by HBM (2 r / bytes-per-value operations a byte for r
+// heads).  Workgroups share the whole batch's work evenly: the tiles of 128
+// tokens of all (sequence, KV head) rows in one list, a contiguous slice of
+// it to each workgroup.  A workgroup finds its slice from the lengths
+// itself, so nothing is read on the host and rows of any lengths balance.
+// A row that lies in one slice is finished there; the pieces of the others
+// are joined by a second kernel.
+//
+// A wave takes 32 tokens of a tile.  S^T = K Q^T on 16x16x32 MFMAs: the A
+// operand of lane l is row (token) l % 16, loaded from the cache straight
+// into registers, and the result has the query head in lane % 16 and tokens
+// 4 (l / 16) + i.  Those are, packed to BF16, the B operand of
+// O^T = V^T P^T with contraction slot 8 (l / 16) + 4 a + i for token
+// 16 a + 4 (l / 16) + i: P never leaves its lane.  The A operand V^T comes
+// from LDS by transposed reads of 4 tokens each.  P is rounded to BF16 (the
+// matrix cores' input type; 2^-9 relative, as the output's own rounding);
+// scores, maxima, sums and outputs are FP32.
+#include "attn.h"
+
+namespace fgg {
+namespace decode_detail {
+
+using namespace attn;
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kWaveTokens = 32;
+constexpr int kTile = kWaves * kWaveTokens;
+constexpr int kMaxHeads = 16;  // query heads of a KV head in one row of work
+
+struct Plan {
+  int total, per;  // tiles of the batch, and of a workgroup
+};
+
+__device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
+  const long long cap = (long long)a.c.width << a.c.page_shift;
+  const int n = a.lengths[b];
+  return n < 0 ? 0 : n > cap ? (int)cap : n;
+}
+// An empty row has a tile too: the one that writes its zeros.
+__device__ __forceinline__ int tiles_of(int len) { return len ? (len + kTile - 1) / kTile : 1; }
+
+// Row of values d0.. of the group's rows of work of a KV head.
+__device__ __forceinline__ int head_groups(const DecodeArgs& a) {
+  return (a.q_heads / a.c.kv_heads + kMaxHeads - 1) / kMaxHeads;
+}
+
+// Tiles before sequence b in one head row, for the sequence that holds tile
+// `pos` of the list (rows = heads of work per sequence).  All threads call.
+struct Place {
+  int b, before;
+};
+__device__ __forceinline__ int scan_lengths(const DecodeArgs& a, int* lds, int& base) {
+  const int per = (a.c.batch + kThreads - 1) / kThreads;
+  const int b0 = threadIdx.x * per, b1 = min(b0 + per, a.c.batch);
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) sum += tiles_of(length_of(a, b));
+  return block_scan<kThreads>(sum, base, lds);
+}
+
+template <int D, bool FP8>
+__global__ __launch_bounds__(kThreads, 2) void decode_kernel(DecodeArgs a) {
+  constexpr int kSteps = D / 32;                // k-steps of a QK product
+  constexpr int kBlocks = D / 16;               // 16-row blocks of O^T
+  constexpr int kRow = D * 2 + 32;              // LDS bytes of a staged V row (BF16)
+  constexpr int kVB = FP8 ? D : D * 2;          // bytes of a cached row
+  constexpr int kLoads = kWaveTokens * kVB / 16 / 64;  // 16-byte pieces of 32 rows per lane
+  constexpr int kLanesPerRow = kVB / 16;
+  constexpr int kOutRow = D + 4;                // floats of a row in the join's LDS
+  constexpr int kStageBytes = kWaves * kWaveTokens * kRow;
+  constexpr int kJoinBytes = kWaves * kMaxHeads * kOutRow * 4;
+  __shared__ __align__(16) uint8_t stage[kStageBytes > kJoinBytes ? kStageBytes : kJoinBytes];
+  __shared__ float ml[kWaves][kMaxHeads][2];
+  __shared__ int scan_lds[kWaves];
+  __shared__ int start_b, start_before;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, quad = lane >> 4;
+  const int groups = head_groups(a);
+  const int group_heads = a.q_heads / a.c.kv_heads;
+  const int rows = a.c.kv_heads * groups;  // rows of work of a sequence
+
+  // this workgroup's slice of the list
+  int base;
+  const int seq_tiles = scan_lengths(a, scan_lds, base);
+  const int total = seq_tiles * rows;
+  const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+  int pos = (int)blockIdx.x * per;
+  const int end = min(total, pos + per);
+  if (pos >= end) return;
+  {
+    const int chunk = (a.c.batch + kThreads - 1) / kThreads;
+    const int b1 = min((tid + 1) * chunk, a.c.batch);
+    int before = base;
+    for (int b = tid * chunk; b < b1; ++b) {
+      const int n = tiles_of(length_of(a, b));
+      if (before * rows <= pos && pos < (before + n) * rows) {
+        start_b = b;
+        start_before = before;
+      }
+      before += n;
+    }
+  }
+  __syncthreads();
+  int b = start_b, before = start_before;
+
+  uint8_t* const my_stage = stage + wave * (kWaveTokens * kRow);
+  while (pos < end) {
+    const int len = length_of(a, b);
+    const int n = tiles_of(len);
+    const int rel = pos - before * rows;
+    const int row = rel / n, t0 = rel - row * n;
+    const int t1 = min(n, t0 + end - pos);
+    const int kvh = row / groups, g0 = (row - kvh * groups) * kMaxHeads;
+    const int heads = min(kMaxHeads, group_heads - g0);
+    const int head0 = kvh * group_heads + g0;
+
+    // Q^T operand: head `col`; the dims of step s, slot 8 quad + j are the
+    // ones that this lane's 16-byte pieces of K hold
+    bf16x8 qf[kSteps];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int d = FP8 ? (s >> 1) * 64 + quad * 16 + (s & 1) * 8 : s * 32 + quad * 8;
+      u32x4 w = {0, 0, 0, 0};
+      if (col < heads)
+        w = *reinterpret_cast<const u32x4*>(a.q + b * a.q_seq + (head0 + col) * a.q_head + d);
+      qf[s] = __builtin_bit_cast(bf16x8, w);
+    }
+    const float kscale = FP8 && a.c.k_scale ? a.c.k_scale[kvh] : 1.0f;
+    const float scale2 = a.scale * kscale * kLog2e;
+    const int32_t* table = a.c.table + b * a.c.table_stride;
+    const uint8_t* kbase = a.c.k + kvh * a.c.k_head;
+    const uint8_t* vbase = a.c.v + kvh * a.c.v_head;
+
+    f32x4 acc[kBlocks];
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) acc[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    float m = kNegInf, l = 0.f;
+
+    for (int t = t0; t < t1; ++t) {
+      const int tok0 = t * kTile + wave * kWaveTokens;
+      if (tok0 >= len) break;
+      // lane L looks up token tok0 + L % 32: its page, or -1
+      const int tok = tok0 + (lane & 31);
+      int page = -1;
+      if (tok < len) {
+        page = table[tok >> a.c.page_shift];
+        if (page >= a.c.num_pages) page = -1;
+      }
+      const uint32_t valid = (uint32_t)__ballot(page >= 0);
+      if (valid == 0) continue;
+      // a token without a page reads page 0 and is masked below
+      const int safe = page < 0 ? 0 : page;
+      const int slot = tok & ((1 << a.c.page_shift) - 1);
+      u32x4 kw[2][kSteps * (FP8 ? 1 : 2) / 2], vw[kLoads];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int src = g * 16 + col;
+        const int pg = __shfl(safe, src, 64), sl = __shfl(slot, src, 64);
+        const uint8_t* p = kbase + pg * a.c.k_page + sl * a.c.k_token + quad * 16;
+#pragma unroll
+        for (int s = 0; s < kVB / 64; ++s) kw[g][s] = *reinterpret_cast<const u32x4*>(p + s * 64);
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int src = i * (64 / kLanesPerRow) + lane / kLanesPerRow;
+        const int pg = __shfl(safe, src, 64), sl = __shfl(slot, src, 64);
+        vw[i] = *reinterpret_cast<const u32x4*>(vbase + pg * a.c.v_page + sl * a.c.v_token +
+                                                (lane % kLanesPerRow) * 16);
+      }
+      // scores
+      float s[8];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          bf16x8 kf;
+          if constexpr (FP8) {
+            const u32x4 w = kw[g][k >> 1];
+            kf = __builtin_bit_cast(bf16x8, fp8x8_to_bf16((u32x2){w[(k & 1) * 2], w[(k & 1) * 2 + 1]}));
+          } else {
+            kf = __builtin_bit_cast(bf16x8, kw[g][k]);
+          }
+          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[k], c, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[g * 4 + i] = c[i] * scale2;
+      }
+      if (valid != 0xFFFFFFFFu) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (!((valid >> ((i >> 2) * 16 + quad * 4 + (i & 3))) & 1)) s[i] = kNegInf;
+        // what the cache holds there may be NaN, and 0 x NaN is not 0
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+          if (!((valid >> (i * (64 / kLanesPerRow) + lane / kLanesPerRow)) & 1))
+            vw[i] = (u32x4){0, 0, 0, 0};
+      }
+      float mx = s[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s[i]);
+      mx = xor_max(xor_max(mx, 16), 32);
+      const float m1 = fmaxf(m, mx);
+      const float ms = m1 == kNegInf ? 0.f : m1;
+      const float alpha = __builtin_amdgcn_exp2f(m - ms);
+      m = m1;
+      float p[8], sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(s[i] - ms);
+        sum += p[i];
+      }
+      l = l * alpha + sum;  // of this lane's tokens; the quads are added at the end
+      const bf16x8 pf = __builtin_bit_cast(
+          bf16x8, (u32x4){pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]),
+                          pack_bf16(p[6], p[7])});
+      // values through LDS (rows of BF16)
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = i * (64 / kLanesPerRow) + lane / kLanesPerRow;
+        uint8_t* dst = my_stage + r * kRow + (lane % kLanesPerRow) * (FP8 ? 32 : 16);
+        if constexpr (FP8) {
+          *reinterpret_cast<u32x4*>(dst) = fp8x8_to_bf16((u32x2){vw[i][0], vw[i][1]});
+          *reinterpret_cast<u32x4*>(dst + 16) = fp8x8_to_bf16((u32x2){vw[i][2], vw[i][3]});
+        } else {
+          *reinterpret_cast<u32x4*>(dst) = vw[i];
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int i = 0; i < kBlocks; ++i) {
+        const uint8_t* src = my_stage + (quad * 4 + (col >> 2)) * kRow + i * 32 + (col & 3) * 8;
+        const u32x2 lo = lds_read_tr(src), hi = lds_read_tr(src + 16 * kRow);
+        const bf16x8 vf = __builtin_bit_cast(bf16x8, (u32x4){lo[0], lo[1], hi[0], hi[1]});
+        acc[i] *= alpha;
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf, acc[i], 0, 0, 0);
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+    l = xor_add(xor_add(l, 16), 32);
+
+    // join the waves
+    __syncthreads();
+    float* ow = reinterpret_cast<float*>(stage) + (wave * kMaxHeads + col) * kOutRow;
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) *reinterpret_cast<f32x4*>(ow + i * 16 + quad * 4) = acc[i];
+    if (quad == 0) {
+      ml[wave][col][0] = m;
+      ml[wave][col][1] = l;
+    }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == n;
+    const int piece = (int)blockIdx.x * 2 + (t0 > 0 ? 0 : 1);
+    {
+      constexpr int kPer = D * kMaxHeads / kThreads;  // outputs of a thread: 8 or 4
+      const int h = tid / (D / kPer), d = (tid % (D / kPer)) * kPer;
+      float M = kNegInf;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) M = fmaxf(M, ml[w][h][0]);
+      const float Ms = M == kNegInf ? 0.f : M;
+      float L = 0.f, o[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) o[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = __builtin_amdgcn_exp2f(ml[w][h][0] - Ms);
+        L += f * ml[w][h][1];
+        const float* src = reinterpret_cast<const float*>(stage) + (w * kMaxHeads + h) * kOutRow + d;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) o[i] += f * src[i];
+      }
+      if (h < heads) {
+        if (whole) {
+          const float vs = FP8 && a.c.v_scale ? a.c.v_scale[kvh] : 1.0f;
+          const float r = L == 0.f ? 0.f : vs / L;
+          uint16_t* out = a.out + ((long long)b * a.q_heads + head0 + h) * D + d;
+#pragma unroll
+          for (int i = 0; i < kPer; i += 4)
+            *reinterpret_cast<uint2*>(out + i) =
+                pack_bf16x4(o[i] * r, o[i + 1] * r, o[i + 2] * r, o[i + 3] * r);
+        } else {
+          float* out = a.part_o + ((long long)piece * kMaxHeads + h) * D + d;
+#pragma unroll
+          for (int i = 0; i < kPer; i += 4)
+            *reinterpret_cast<f32x4*>(out + i) = (f32x4){o[i], o[i + 1], o[i + 2], o[i + 3]};
+          if (d == 0) {
+            a.part_ml[(piece * kMaxHeads + h) * 2] = M;
+            a.part_ml[(piece * kMaxHeads + h) * 2 + 1] = L;
+          }
+        }
+      }
+    }
+    __syncthreads();  // the stage is free again
+    pos += t1 - t0;
+    if (t1 == n && row == rows - 1) {
+      before += n;
+      ++b;
+    }
+  }
+}
+
+// Joins the pieces of the rows that the slices of several workgroups share.
+// One workgroup per query head and sequence; the pieces go to groups of D / 4
+// lanes in turn.
+template <int D>
+__global__ __launch_bounds__(kThreads) void join_kernel(DecodeArgs a, int workgroups) {
+  constexpr int kLanes = D / 4, kSets = kThreads / kLanes;
+  __shared__ int scan_lds[kWaves];
+  __shared__ int my_before;
+  __shared__ float red_m[kWaves];
+  __shared__ __align__(16) float red_o[kSets][D];
+  __shared__ float red_l[kSets];
+  const int tid = threadIdx.x;
+  const int b = (int)blockIdx.x / a.q_heads, h = (int)blockIdx.x % a.q_heads;
+  const int group_heads = a.q_heads / a.c.kv_heads, groups = head_groups(a);
+  const int rows = a.c.kv_heads * groups;
+  const int n = tiles_of(length_of(a, b));
+  if (n == 1) return;
+  int base;
+  const int total = scan_lengths(a, scan_lds, base) * rows;
+  {
+    const int chunk = (a.c.batch + kThreads - 1) / kThreads;
+    if (b >= tid * chunk && b < (tid + 1) * chunk) {
+      int before = base;
+      for (int i = tid * chunk; i < b; ++i) before += tiles_of(length_of(a, i));
+      my_before = before;
+    }
+  }
+  __syncthreads();
+  const int per = (total + workgroups - 1) / workgroups;
+  const int kvh = h / group_heads, hh = h - kvh * group_heads;
+  const int s0 = my_before * rows + (kvh * groups + hh / kMaxHeads) * n, s1 = s0 + n;
+  const int first = s0 / per, last = (s1 - 1) / per;
+  if (first == last) return;  // one workgroup had the whole row
+  const int hr = hh % kMaxHeads;
+  // piece of workgroup w: slot 0 if the row began before its slice
+  auto piece_of = [&](int w) { return (w * 2 + (s0 < w * per ? 0 : 1)) * kMaxHeads + hr; };
+  float m = kNegInf;
+  for (int w = first + tid; w <= last; w += kThreads) m = fmaxf(m, a.part_ml[piece_of(w) * 2]);
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) m = xor_max(m, off);
+  if ((tid & 63) == 0) red_m[tid >> 6] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) m = fmaxf(m, red_m[w]);
+  const float ms = m == kNegInf ? 0.f : m;
+  const int set = tid / kLanes, d = (tid % kLanes) * 4;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  float l = 0.f;
+  for (int w = first + set; w <= last; w += kSets) {
+    const int p = piece_of(w);
+    const float f = __builtin_amdgcn_exp2f(a.part_ml[p * 2] - ms);
+    l += f * a.part_ml[p * 2 + 1];
+    o += f * *reinterpret_cast<const f32x4*>(a.part_o + (long long)p * D + d);
+  }
+  *reinterpret_cast<f32x4*>(&red_o[set][d]) = o;
+  if (d == 0) red_l[set] = l;
+  __syncthreads();
+  if (tid < kLanes) {
+    float L = 0.f;
+    f32x4 r = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kSets; ++i) {
+      L += red_l[i];
+      r += *reinterpret_cast<const f32x4*>(&red_o[i][tid * 4]);
+    }
+    const float vs = a.c.fp8 && a.c.v_scale ? a.c.v_scale[kvh] : 1.0f;
+    r *= L == 0.f ? 0.f : vs / L;
+    *reinterpret_cast<uint2*>(a.out + ((long long)b * a.q_heads + h) * D + tid * 4) =
+        pack_bf16x4(r[0], r[1], r[2], r[3]);
+  }
+}
+
+template <int D>
+hipError_t launch(const DecodeArgs& a, int workgroups, hipStream_t s) {
+  if (a.c.fp8)
+    hipLaunchKernelGGL((decode_kernel<D, true>), dim3(workgroups), dim3(kThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((decode_kernel<D, false>), dim3(workgroups), dim3(kThreads), 0, s, a);
+  hipError_t e = hipGetLastError();
+  // a row of one tile is never split: tables that hold no more need no join
+  if (e != hipSuccess || ((long long)a.c.width << a.c.page_shift) <= kTile) return e;
+  hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)(a.c.batch * a.q_heads)), dim3(kThreads), 0, s, a,
+                     workgroups);
+  return hipGetLastError();
+}
+
+}  // namespace decode_detail
+
+using namespace decode_detail;
+
+int decode_workgroups(int batch, int q_heads, int kv_heads, long long max_len, int num_cus) {
+  const long long groups = (q_heads / kv_heads + kMaxHeads - 1) / kMaxHeads;
+  const long long tiles = (long long)batch * kv_heads * groups * ((max_len + kTile - 1) / kTile);
+  const long long cap = 2LL * num_cus;
+  return (int)(tiles < 1 ? 1 : tiles < cap ? tiles : cap);
+}
+
+size_t decode_workspace(int workgroups, int D) {
+  return (size_t)workgroups * 2 * kMaxHeads * (D + 2) * sizeof(float);
+}
+
+hipError_t launch_decode(const DecodeArgs& a, int workgroups, hipStream_t s) {
+  return a.D == 64 ? launch<64>(a, workgroups, s) : launch<128>(a, workgroups, s);
+}
+
+}  // namespace fgg

@@ -37,6 +37,7 @@
 #ifndef FGG_H
 #define FGG_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -434,6 +435,114 @@ int fgg_tuned_tile(int kind, int M, int N, int K, int G);
 
 /* Forget every recorded choice. */
 void fgg_tune_clear(void);
+
+/* ------------------------------------------------------------------------
+ * Attention of the layers around the experts: the append of new keys and
+ * values to a paged cache, one new token a sequence against that cache, and
+ * whole prompts.
+ *
+ * A paged cache holds K and V in num_pages pages of page_size tokens of
+ * kv_heads heads of head_dim values.  Sequence b's token t lives in page
+ * page_table[b, t / page_size], slot t % page_size.  A table entry outside
+ * [0, num_pages) is no page: nothing is written there, and its tokens are
+ * not attended to.  k_strides and v_strides are in values between pages,
+ * heads and tokens, in any order of these three (head_dim is contiguous):
+ * both [pages, heads, tokens, dim] and [pages, tokens, heads, dim] pools
+ * are described as they are, and K and V may share a pool.
+ * ------------------------------------------------------------------------ */
+#define FGG_KV_BF16 0
+#define FGG_KV_E4M3 1
+
+typedef struct {
+  void* k;                   /* device */
+  void* v;                   /* device */
+  const float* k_scale;      /* [kv_heads], or NULL (1): E4M3 only; a stored   */
+  const float* v_scale;      /*   code stands for its value times the scale    */
+  const int32_t* page_table; /* [batch, table_width], rows table_stride apart  */
+  long long table_stride;    /* in entries                                     */
+  long long k_strides[3];    /* page, head, token; multiples of 16 bytes       */
+  long long v_strides[3];
+  int dtype;                 /* FGG_KV_BF16 or FGG_KV_E4M3                     */
+  int num_pages, kv_heads;
+  int page_size;             /* a power of two, at most 2^16                   */
+  int head_dim;              /* 64 or 128                                      */
+  int batch, table_width;
+} fgg_kv_cache;
+
+/*
+ * rope_kv_append -- rotate the queries and keys of T new tokens by their
+ * positions and write keys and values to the cache.
+ *
+ *   q, k, v    BF16 [T, heads, head_dim], read at strides = {q token, q head,
+ *              k token, k head, v token, v head} in values (multiples of 8)
+ *   turns      float32 [num_turns, rot_dim]: row p holds the cosines of
+ *              position p's rot_dim / 2 angles, then their sines
+ *   positions  [T] int32: token t's position, which is also its place in
+ *              its sequence.  A token whose position is negative, at least
+ *              num_turns or past the table's end, or whose sequence is
+ *              outside [0, batch), is padding: nothing is written to the
+ *              cache and its rows of q_out and k_out are zeros.
+ *   seq_ids    [T] int32: token t's row of the page table; NULL: row t
+ *              (T = batch)
+ *   q_out      BF16 [T, q_heads, head_dim], the rotated queries
+ *   k_out      BF16 [T, kv_heads, head_dim], the rotated keys, or NULL
+ *
+ * Pair i < rot_dim / 2 of a head is values (i, i + rot_dim / 2), or
+ * (2 i, 2 i + 1) if interleaved is not 0; values from rot_dim on are copied.
+ * FP32, then one rounding to nearest even: to BF16, or for an E4M3 cache
+ * E4M3FN(clamp(x / scale, +-448)) (NaN stays NaN).  Scales must be positive.
+ * Two tokens with the same place leave either's values there.
+ * rot_dim: a multiple of 16 (an even one that is not: FGG_EUNSUPPORTED).
+ */
+fgg_status rope_kv_append(const fgg_kv_cache* cache, const void* q, const void* k, const void* v,
+                          const long long* strides, const float* turns, int num_turns, int rot_dim,
+                          int interleaved, const int32_t* positions, const int32_t* seq_ids,
+                          void* q_out, void* k_out, int T, int q_heads, void* stream);
+
+/*
+ * paged_decode_attention -- attention of one new token a sequence over the
+ * cached tokens [0, lengths[b]) of its sequence:
+ *
+ *   out[b, h] = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q[b, h] . k_t),
+ *   query head h reading KV head h / (q_heads / kv_heads).
+ *
+ *   q        BF16 [batch, q_heads, head_dim] at the given strides
+ *   lengths  [batch] int32, clamped to [0, table_width * page_size]; read on
+ *            the device only.  No token to attend to: zeros.
+ *   out      BF16 [batch, q_heads, head_dim]
+ *   workspace  device memory of at least the bytes that
+ *            paged_decode_attention_workspace gives for this cache (its
+ *            sizes only: no pointer is read) and q_heads, 16-byte aligned; its
+ *            contents need no initialisation and are free after the call's
+ *            work on `stream` is done.
+ *
+ * Scores, maxima, sums and outputs are FP32; the weights p_t are rounded to
+ * BF16 for the product with V.  What the cache holds past a sequence's
+ * length never reaches an output, NaN included.
+ */
+fgg_status paged_decode_attention_workspace(const fgg_kv_cache* cache, int q_heads, size_t* bytes);
+fgg_status paged_decode_attention(const fgg_kv_cache* cache, const void* q, long long q_seq_stride,
+                                  long long q_head_stride, const int32_t* lengths, float scale,
+                                  void* out, int q_heads, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/*
+ * prompt_attention -- causal attention over whole prompts packed one after
+ * the other: token t of a prompt attends to its tokens [0, t].
+ *
+ *   q, k, v  BF16 [T, heads, head_dim] at strides = {q token, q head, k
+ *            token, k head, v token, v head} in values (multiples of 8)
+ *   starts   [batch + 1] int32, non-decreasing: prompt i is tokens
+ *            [starts[i], starts[i + 1]) (clamped to [0, T]); read on the
+ *            device only.  Tokens of no prompt get zeros.
+ *   out      BF16 [T, q_heads, head_dim]
+ *
+ * Arithmetic as paged_decode_attention; keys and values that a query does
+ * not attend to never reach its output, infinities and NaN included.
+ */
+fgg_status prompt_attention(const void* q, const void* k, const void* v, const long long* strides,
+                            const int32_t* starts, float scale, void* out, int T, int batch,
+                            int q_heads, int kv_heads, int head_dim, void* stream);
 
 /* Device facts cached once per device (gfx950 check, CU count, LDS bytes per
  * workgroup).  Returns FGG_EDEVICE when no usable device is present. */
