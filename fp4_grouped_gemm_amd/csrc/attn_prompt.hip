@@ -33,6 +33,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kRows = 32 * kWaves;  // queries of a workgroup
 constexpr int kKeys = 64;           // keys of a tile
+constexpr float kSlack = 8.f;       // weights may reach 2^kSlack before a rescaling
 
 // Segment i of the packed tokens: 0 is what lies before the first prompt,
 // 1 .. batch the prompts, batch + 1 what lies after the last.  Every bound is
@@ -53,15 +54,30 @@ __device__ __forceinline__ bool any_odd(u32x4 w) {
   return odd;
 }
 
+// LDS layout of a staged tile: row r at r D 2 bytes, its 16-byte chunk c at
+// chunk c ^ key(r), so that what one cycle of a fragment read touches lies in
+// different banks.  K: 16 lanes read one chunk index of 16 rows that differ in
+// their low four bits.  V (transposed reads): groups of lanes read 64 bytes
+// of four consecutive rows, or 32 bytes of eight.
+template <int D>
+__device__ __forceinline__ int k_key(int r) {
+  return D == 128 ? r & 15 : (r >> 1) & 7;
+}
+template <int D>
+__device__ __forceinline__ int v_key(int r) {
+  return D == 128 ? ((r & 3) << 2) | ((r >> 1) & 2) : ((r << 1) & 4) | ((r >> 1) & 2);
+}
+
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
-  constexpr int kSteps = D / 16;   // k-steps of a QK product
-  constexpr int kBlocks = D / 32;  // 32-row blocks of O^T
-  constexpr int kKRow = D * 2 + 16, kVRow = D * 2 + 32;  // LDS bytes of a staged row
-  constexpr int kLanesPerRow = D / 8;
-  constexpr int kLoads = kKeys * kLanesPerRow / kThreads;  // 16-byte pieces of a tile per thread
-  __shared__ __align__(16) uint8_t ks[kKeys * kKRow];
-  __shared__ __align__(16) uint8_t vs[kKeys * kVRow];
+  constexpr int kSteps = D / 16;    // k-steps of a QK product
+  constexpr int kBlocks = D / 32;   // 32-row blocks of O^T
+  constexpr int kRowBytes = D * 2;
+  constexpr int kTileBytes = kKeys * kRowBytes;
+  constexpr int kChunks = D / 8;    // 16-byte chunks of a row
+  constexpr int kLoads = kTileBytes / 16 / kThreads;  // chunks of a tile per thread
+  // two tiles each of K and V: one is read while the next one lands
+  __shared__ __align__(16) uint8_t lds[2][2][kTileBytes];
   __shared__ int scan_lds[kWaves];
   __shared__ int my_seg, my_tile;
   __shared__ int odd_tile;  // first key + 1 of the last tile with a value that is not finite
@@ -103,7 +119,8 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
   if (seg < 0) return;
   int lo, hi;
   segment(a, seg, lo, hi);
-  const int len = hi - lo;
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  const int len = __builtin_amdgcn_readfirstlane(hi) - lo;
   const int r0 = __builtin_amdgcn_readfirstlane(my_tile) * kRows;
   const int w0 = r0 + wave * 32;  // this wave's first query
   const int query = w0 + col;
@@ -114,10 +131,15 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
   for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
     for (int j = 0; j < 16; ++j) acc[i][j] = 0.f;
+  // the running maximum (of the scores before scaling) and sum
   float m = kNegInf, l = 0.f;
 
   if (real) {
-    const float scale2 = a.scale * kLog2e;
+    // a negative scale goes into the queries' signs, so that the largest
+    // product is the largest score; and no scale is 0, which would make NaN
+    // of a masked score (weights differ from those of 0 by 1e-30)
+    const float scale2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
     bf16x8 qf[kSteps];
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
@@ -125,51 +147,66 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
       if (query < len)
         w = *reinterpret_cast<const u32x4*>(a.q + (long long)(lo + query) * a.q_token +
                                             head * a.q_head + s * 16 + half * 8);
-      qf[s] = __builtin_bit_cast(bf16x8, w);
+      qf[s] = __builtin_bit_cast(bf16x8, w ^ flip);
     }
     const uint16_t* kp = a.k + (long long)lo * a.k_token + kvh * a.k_head;
     const uint16_t* vp = a.v + (long long)lo * a.v_token + kvh * a.v_head;
     const int keys = min(len, r0 + kRows);  // that any query of the workgroup sees
-    u32x4 kw[kLoads], vw[kLoads];
-    auto load = [&](int k0) {
+
+    // Staging: load i of a wave fills 64 chunks, rows of kChunks, in LDS
+    // order; a lane fetches the chunk that belongs at its place.  Rows past
+    // the last key are past the resource's end and read as zeros.
+    const int row_in = (wave * 64 + lane) / kChunks, chunk_in = lane % kChunks;
+    constexpr int kRowsPerLoad = kThreads / kChunks;
+    const uint32_t k_off = (uint32_t)(row_in * a.k_token * 2), v_off = (uint32_t)(row_in * a.v_token * 2);
+    const uint32_t lds0 = lds_dma::lds_addr(&lds[0][0][0]) + wave * 1024;
+    auto stage = [&](int k0, int buf) {
+      const int left = min(keys - k0, kKeys);
+      const i32x4 kr = lds_dma::rsrc(kp + (long long)k0 * a.k_token,
+                                     (uint32_t)(((long long)(left - 1) * a.k_token + D) * 2));
+      const i32x4 vr = lds_dma::rsrc(vp + (long long)k0 * a.v_token,
+                                     (uint32_t)(((long long)(left - 1) * a.v_token + D) * 2));
+      const uint32_t at = lds0 + buf * (2 * kTileBytes);
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int r = k0 + i * (kThreads / kLanesPerRow) + tid / kLanesPerRow;
-        const int c = (tid % kLanesPerRow) * 8;
-        kw[i] = vw[i] = (u32x4){0, 0, 0, 0};
-        if (r < keys) {
-          kw[i] = *reinterpret_cast<const u32x4*>(kp + (long long)r * a.k_token + c);
-          vw[i] = *reinterpret_cast<const u32x4*>(vp + (long long)r * a.v_token + c);
-        }
+        const int r = row_in + i * kRowsPerLoad;
+        const uint32_t rows = (uint32_t)(i * kRowsPerLoad);
+        const bool in = r < left;
+        lds_dma::dma16(kr, at + i * (kThreads * 16),
+                       in ? k_off + rows * (uint32_t)a.k_token * 2 + ((chunk_in ^ k_key<D>(r)) << 4)
+                          : lds_dma::kSkip, 0);
+        lds_dma::dma16(vr, at + kTileBytes + i * (kThreads * 16),
+                       in ? v_off + rows * (uint32_t)a.v_token * 2 + ((chunk_in ^ v_key<D>(r)) << 4)
+                          : lds_dma::kSkip, 0);
       }
     };
-    load(0);
-    for (int k0 = 0; k0 < keys; k0 += kKeys) {
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int r = i * (kThreads / kLanesPerRow) + tid / kLanesPerRow;
-        const int c = (tid % kLanesPerRow) * 16;
-        *reinterpret_cast<u32x4*>(ks + r * kKRow + c) = kw[i];
-        *reinterpret_cast<u32x4*>(vs + r * kVRow + c) = vw[i];
-      }
+    // LDS offsets of this lane's fragment reads, less what steps add
+    const int v_row = half * 4 + ((lane & 15) >> 2);
+
+    stage(0, 0);
+    for (int k0 = 0, buf = 0; k0 < keys; k0 += kKeys, buf ^= 1) {
+      lds_dma::wait_vmem<0>();
+      lds_dma::lds_barrier();
+      if (k0 + kKeys < keys) stage(k0 + kKeys, buf ^ 1);
+      const uint8_t* ks = lds[buf][0];
+      uint8_t* vs = lds[buf][1];
       const bool diagonal = k0 + kKeys - 1 > r0;
+      bool odd = false;
       if (diagonal) {
-        bool odd = false;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) odd |= any_odd(vw[i]);
+        for (int i = 0; i < kLoads; ++i)
+          odd |= any_odd(*reinterpret_cast<const u32x4*>(vs + (i * kThreads + tid) * 16));
         if (odd) odd_tile = k0 + 1;
-      }
-      __syncthreads();
-      const bool odd = diagonal && odd_tile == k0 + 1;
-      if (odd) {
-        for (int x = tid; x < kKeys * D; x += kThreads) {
-          uint16_t* w = reinterpret_cast<uint16_t*>(vs + (x / D) * kVRow) + x % D;
-          if ((*w & 0x7F80u) == 0x7F80u) *w = 0;
+        lds_dma::lds_barrier();
+        odd = odd_tile == k0 + 1;
+        if (odd) {
+          for (int x = tid; x < kKeys * D; x += kThreads) {
+            uint16_t* w = reinterpret_cast<uint16_t*>(vs) + x;
+            if ((*w & 0x7F80u) == 0x7F80u) *w = 0;
+          }
+          lds_dma::lds_barrier();
         }
-        __syncthreads();
       }
-      if (k0 + kKeys < keys) load(k0 + kKeys);
       if (k0 > w0 + 31) continue;  // every key lies after every query of the wave
       f32x16 s[2];
 #pragma unroll
@@ -178,15 +215,12 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
         for (int j = 0; j < 16; ++j) s[b][j] = 0.f;
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
-          const bf16x8 kf = *reinterpret_cast<const bf16x8*>(ks + (b * 32 + col) * kKRow + k * 32 +
-                                                             half * 16);
+          const int r = b * 32 + col;
+          const bf16x8 kf = *reinterpret_cast<const bf16x8*>(
+              ks + r * kRowBytes + (((2 * k + half) ^ k_key<D>(r)) << 4));
           s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[k], s[b], 0, 0, 0);
         }
       }
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) s[b][j] *= scale2;
       if (k0 + kKeys - 1 > w0) {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -200,11 +234,19 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) mx = fmaxf(mx, s[b][j]);
       mx = xor_max(mx, 32);
-      const float m1 = fmaxf(m, mx);
-      const float ms = m1 == kNegInf ? 0.f : m1;
-      const float alpha = __builtin_amdgcn_exp2f(m - ms);
-      m = m1;
-      float sum = 0.f;
+      // The subtrahend follows the maximum only when that would let a weight
+      // pass 2^kSlack: the outputs are then scaled down, which late tiles
+      // almost never need.  A query's result depends on its own scores only.
+      const bool grown = (mx - m) * scale2 > kSlack;
+      if (__any(grown)) {
+        const float alpha = grown ? __builtin_amdgcn_exp2f((m - mx) * scale2) : 1.f;
+        m = grown ? mx : m;
+        l *= alpha;
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) acc[i] *= alpha;
+      }
+      const float ms = m == kNegInf ? 0.f : m * scale2;
+      float sum0 = 0.f, sum1 = 0.f;
       bf16x8 pf[2][2];
 #pragma unroll
       for (int b = 0; b < 2; ++b)
@@ -212,26 +254,31 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
         for (int k = 0; k < 2; ++k) {
           float p[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            p[j] = __builtin_amdgcn_exp2f(s[b][k * 8 + j] - ms);
-            sum += p[j];
+          for (int j = 0; j < 8; ++j) p[j] = __builtin_amdgcn_exp2f(fmaf(s[b][k * 8 + j], scale2, -ms));
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            sum0 += p[j];
+            sum1 += p[j + 1];
           }
           pf[b][k] = __builtin_bit_cast(
               bf16x8, (u32x4){pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]),
                               pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7])});
         }
-      l = l * alpha + sum;
+      l += sum0 + sum1;
 #pragma unroll
       for (int i = 0; i < kBlocks; ++i) {
-        acc[i] *= alpha;
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const uint8_t* src = vs + (b * 32 + k * 16 + half * 4 + ((lane & 15) >> 2)) * kVRow +
-                                 i * 64 + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
-            const u32x2 x = lds_read_tr(src), y = lds_read_tr(src + 8 * kVRow);
-            const bf16x8 vf = __builtin_bit_cast(bf16x8, (u32x4){x[0], x[1], y[0], y[1]});
+            u32x2 x[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int r = b * 32 + k * 16 + e * 8 + v_row;
+              const int c = i * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+              x[e] = lds_read_tr(vs + r * kRowBytes + ((c ^ v_key<D>(r)) << 4) + (lane & 1) * 8);
+            }
+            const bf16x8 vf = __builtin_bit_cast(bf16x8, (u32x4){x[0][0], x[0][1], x[1][0], x[1][1]});
             acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[b][k], acc[i], 0, 0, 0);
           }
       }
