@@ -24,6 +24,8 @@
 // to the queries that see them.
 #include "attn.h"
 
+#include <type_traits>
+
 namespace fgg {
 namespace prompt_detail {
 
@@ -68,19 +70,25 @@ __device__ __forceinline__ int v_key(int r) {
   return D == 128 ? ((r & 3) << 2) | ((r >> 1) & 2) : ((r << 1) & 4) | ((r >> 1) & 2);
 }
 
+// Maximum over a lane and its partner in the other half of the wave.
+__device__ __forceinline__ float half_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
   constexpr int kSteps = D / 16;    // k-steps of a QK product
   constexpr int kBlocks = D / 32;   // 32-row blocks of O^T
   constexpr int kRowBytes = D * 2;
-  constexpr int kTileBytes = kKeys * kRowBytes;
+  constexpr int kBlockBytes = 32 * kRowBytes;  // of a block of 32 keys
   constexpr int kChunks = D / 8;    // 16-byte chunks of a row
-  constexpr int kLoads = kTileBytes / 16 / kThreads;  // chunks of a tile per thread
-  // two tiles each of K and V: one is read while the next one lands
-  __shared__ __align__(16) uint8_t lds[2][2][kTileBytes];
+  constexpr int kLoads = kBlockBytes / 16 / kThreads;  // chunks of a block per thread
+  // rings of four blocks of K and four of V: two are read while two land
+  __shared__ __align__(16) uint8_t lds[8 * kBlockBytes];
   __shared__ int scan_lds[kWaves];
   __shared__ int my_seg, my_tile;
-  __shared__ int odd_tile;  // first key + 1 of the last tile with a value that is not finite
+  __shared__ int odd_tile;  // 1 + the diagonal tile found to hold a value that is not finite
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -156,87 +164,59 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
     // Staging: load i of a wave fills 64 chunks, rows of kChunks, in LDS
     // order; a lane fetches the chunk that belongs at its place.  Rows past
     // the last key are past the resource's end and read as zeros.
-    const int row_in = (wave * 64 + lane) / kChunks, chunk_in = lane % kChunks;
+    const int row_in = tid / kChunks, chunk_in = tid % kChunks;
     constexpr int kRowsPerLoad = kThreads / kChunks;
     const uint32_t k_off = (uint32_t)(row_in * a.k_token * 2), v_off = (uint32_t)(row_in * a.v_token * 2);
-    const uint32_t lds0 = lds_dma::lds_addr(&lds[0][0][0]) + wave * 1024;
-    auto stage = [&](int k0, int buf) {
-      const int left = min(keys - k0, kKeys);
-      const i32x4 kr = lds_dma::rsrc(kp + (long long)k0 * a.k_token,
-                                     (uint32_t)(((long long)(left - 1) * a.k_token + D) * 2));
-      const i32x4 vr = lds_dma::rsrc(vp + (long long)k0 * a.v_token,
-                                     (uint32_t)(((long long)(left - 1) * a.v_token + D) * 2));
-      const uint32_t at = lds0 + buf * (2 * kTileBytes);
+    const uint32_t lds0 = lds_dma::lds_addr(lds) + wave * 1024;
+    auto stage = [&](const uint16_t* p, long long stride, uint32_t off, bool value, int block) __attribute__((always_inline)) {
+      const int left = min(keys - block * 32, 32);
+      const i32x4 rs = lds_dma::rsrc(p + (long long)block * 32 * stride,
+                                     left > 0 ? (uint32_t)((left - 1) * (uint32_t)stride + D) * 2 : 0u);
+      const uint32_t at = lds0 + ((value ? 4 : 0) + (block & 3)) * kBlockBytes;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int r = row_in + i * kRowsPerLoad;
-        const uint32_t rows = (uint32_t)(i * kRowsPerLoad);
-        const bool in = r < left;
-        lds_dma::dma16(kr, at + i * (kThreads * 16),
-                       in ? k_off + rows * (uint32_t)a.k_token * 2 + ((chunk_in ^ k_key<D>(r)) << 4)
-                          : lds_dma::kSkip, 0);
-        lds_dma::dma16(vr, at + kTileBytes + i * (kThreads * 16),
-                       in ? v_off + rows * (uint32_t)a.v_token * 2 + ((chunk_in ^ v_key<D>(r)) << 4)
-                          : lds_dma::kSkip, 0);
+        const int c = chunk_in ^ (value ? v_key<D>(r) : k_key<D>(r));
+        lds_dma::dma16(rs, at + i * (kThreads * 16),
+                       r < left ? off + (uint32_t)(i * kRowsPerLoad) * (uint32_t)stride * 2 + (c << 4)
+                                : lds_dma::kSkip, 0);
       }
     };
-    // LDS offsets of this lane's fragment reads, less what steps add
+    auto stage_k = [&](int block) __attribute__((always_inline)) { stage(kp, a.k_token, k_off, false, block); };
+    auto stage_v = [&](int block) __attribute__((always_inline)) { stage(vp, a.v_token, v_off, true, block); };
     const int v_row = half * 4 + ((lane & 15) >> 2);
 
-    stage(0, 0);
-    for (int k0 = 0, buf = 0; k0 < keys; k0 += kKeys, buf ^= 1) {
-      lds_dma::wait_vmem<0>();
-      lds_dma::lds_barrier();
-      if (k0 + kKeys < keys) stage(k0 + kKeys, buf ^ 1);
-      const uint8_t* ks = lds[buf][0];
-      uint8_t* vs = lds[buf][1];
-      const bool diagonal = k0 + kKeys - 1 > r0;
-      bool odd = false;
-      if (diagonal) {
+    // The steps of a block of 32 keys: its scores, the largest one, the
+    // weights, their product with the values.  `block` (a constant) counts the
+    // four blocks of the two tiles in LDS.
+    float mx;
+    auto scores = [&](auto block, f32x16& s) __attribute__((always_inline)) {
+      const uint8_t* ks = lds + block * kBlockBytes;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-          odd |= any_odd(*reinterpret_cast<const u32x4*>(vs + (i * kThreads + tid) * 16));
-        if (odd) odd_tile = k0 + 1;
-        lds_dma::lds_barrier();
-        odd = odd_tile == k0 + 1;
-        if (odd) {
-          for (int x = tid; x < kKeys * D; x += kThreads) {
-            uint16_t* w = reinterpret_cast<uint16_t*>(vs) + x;
-            if ((*w & 0x7F80u) == 0x7F80u) *w = 0;
-          }
-          lds_dma::lds_barrier();
-        }
+      for (int j = 0; j < 16; ++j) s[j] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        const bf16x8 kf = *reinterpret_cast<const bf16x8*>(
+            ks + col * kRowBytes + (((2 * k + half) ^ k_key<D>(col)) << 4));
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[k], s, 0, 0, 0);
       }
-      if (k0 > w0 + 31) continue;  // every key lies after every query of the wave
-      f32x16 s[2];
+    };
+    // keys after the query, in the block that starts with the wave's first one
+    auto hide = [&](f32x16& s) __attribute__((always_inline)) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int j = 0; j < 16; ++j)
+        if ((j & 3) + 8 * (j >> 2) + 4 * half > col) s[j] = kNegInf;
+    };
+    auto largest = [&](const f32x16& s) __attribute__((always_inline)) {
+      float x = s[0];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) s[b][j] = 0.f;
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          const int r = b * 32 + col;
-          const bf16x8 kf = *reinterpret_cast<const bf16x8*>(
-              ks + r * kRowBytes + (((2 * k + half) ^ k_key<D>(r)) << 4));
-          s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[k], s[b], 0, 0, 0);
-        }
-      }
-      if (k0 + kKeys - 1 > w0) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (k0 + b * 32 + (j & 3) + 8 * (j >> 2) + 4 * half > query) s[b][j] = kNegInf;
-      }
-      float mx = kNegInf;
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) mx = fmaxf(mx, s[b][j]);
-      mx = xor_max(mx, 32);
-      // The subtrahend follows the maximum only when that would let a weight
-      // pass 2^kSlack: the outputs are then scaled down, which late tiles
-      // almost never need.  A query's result depends on its own scores only.
+      for (int j = 1; j < 16; ++j) x = fmaxf(x, s[j]);
+      return half_max(x);
+    };
+    // The subtrahend follows the maximum only when that would let a weight
+    // pass 2^kSlack: the outputs are then scaled down, which late blocks
+    // almost never need.  A query's result depends on its own scores only.
+    auto follow = [&]() __attribute__((always_inline)) {
       const bool grown = (mx - m) * scale2 > kSlack;
       if (__any(grown)) {
         const float alpha = grown ? __builtin_amdgcn_exp2f((m - mx) * scale2) : 1.f;
@@ -245,56 +225,138 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i) acc[i] *= alpha;
       }
+    };
+    auto weights = [&](const f32x16& s, bf16x8 (&pf)[2]) __attribute__((always_inline)) {
       const float ms = m == kNegInf ? 0.f : m * scale2;
       float sum0 = 0.f, sum1 = 0.f;
-      bf16x8 pf[2][2];
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int k = 0; k < 2; ++k) {
+        float p[8];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float p[8];
+        for (int j = 0; j < 8; ++j) p[j] = __builtin_amdgcn_exp2f(fmaf(s[k * 8 + j], scale2, -ms));
 #pragma unroll
-          for (int j = 0; j < 8; ++j) p[j] = __builtin_amdgcn_exp2f(fmaf(s[b][k * 8 + j], scale2, -ms));
-#pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            sum0 += p[j];
-            sum1 += p[j + 1];
-          }
-          pf[b][k] = __builtin_bit_cast(
-              bf16x8, (u32x4){pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]),
-                              pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7])});
+        for (int j = 0; j < 8; j += 2) {
+          sum0 += p[j];
+          sum1 += p[j + 1];
         }
+        pf[k] = __builtin_bit_cast(bf16x8, (u32x4){pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]),
+                                                   pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7])});
+      }
       l += sum0 + sum1;
+    };
+    auto add_values = [&](auto block, const bf16x8 (&pf)[2]) __attribute__((always_inline)) {
+      const uint8_t* vs = lds + (4 + block) * kBlockBytes;
 #pragma unroll
-      for (int i = 0; i < kBlocks; ++i) {
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int i = 0; i < kBlocks; ++i) {
+          u32x2 x[2];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            u32x2 x[2];
+          for (int e = 0; e < 2; ++e) {
+            const int r = k * 16 + e * 8 + v_row;
+            const int c = i * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+            x[e] = lds_read_tr(vs + r * kRowBytes + ((c ^ v_key<D>(r)) << 4) + (lane & 1) * 8);
+          }
+          const bf16x8 vf = __builtin_bit_cast(bf16x8, (u32x4){x[0][0], x[0][1], x[1][0], x[1][1]});
+          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[k], acc[i], 0, 0, 0);
+        }
+    };
+    auto add_odd = [&](int k0) __attribute__((always_inline)) {
+      for (int u = k0; u <= min(query, k0 + kKeys - 1); ++u) {
+        const uint16_t* v = vp + (long long)u * a.v_token;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int r = b * 32 + k * 16 + e * 8 + v_row;
-              const int c = i * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-              x[e] = lds_read_tr(vs + r * kRowBytes + ((c ^ v_key<D>(r)) << 4) + (lane & 1) * 8);
-            }
-            const bf16x8 vf = __builtin_bit_cast(bf16x8, (u32x4){x[0][0], x[0][1], x[1][0], x[1][1]});
-            acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[b][k], acc[i], 0, 0, 0);
+        for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const uint32_t w = v[i * 32 + (j & 3) + 8 * (j >> 2) + 4 * half];
+            if ((w & 0x7F80u) == 0x7F80u) acc[i][j] += __uint_as_float(w << 16);
           }
       }
-      if (odd && query < len) {
-        for (int u = k0; u <= min(query, k0 + kKeys - 1); ++u) {
-          const uint16_t* v = vp + (long long)u * a.v_token;
-#pragma unroll
-          for (int i = 0; i < kBlocks; ++i)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const uint32_t w = v[i * 32 + (j & 3) + 8 * (j >> 2) + 4 * half];
-              if ((w & 0x7F80u) == 0x7F80u) acc[i][j] += __uint_as_float(w << 16);
-            }
-        }
-      }
+    };
+
+    // Takes the scores of a block through softmax and values while it computes
+    // those of the next one: matrix and vector work of one wave that do not
+    // wait for each other.
+    auto step = [&](auto block, f32x16& s, f32x16& next) __attribute__((always_inline)) {
+      follow();
+      bf16x8 pf[2];
+      scores(std::integral_constant<int, (block + 1) % 4>{}, next);
+      weights(s, pf);
+      add_values(block, pf);
+      mx = largest(next);
+    };
+    // Landed after this: V of blocks u and u + 1, K of u + 1 and u + 2; every
+    // wave is done with the blocks before those, whose places the next ones
+    // take.
+    auto turn = [&](int u) __attribute__((always_inline)) {
+      lds_dma::wait_vmem<0>();
+      lds_dma::lds_barrier();
+      stage_v(u + 2);
+      stage_v(u + 3);
+      stage_k(u + 3);
+      stage_k(u + 4);
+    };
+    constexpr std::integral_constant<int, 0> kB0;
+    constexpr std::integral_constant<int, 1> kB1;
+    constexpr std::integral_constant<int, 2> kB2;
+    constexpr std::integral_constant<int, 3> kB3;
+    f32x16 s0, s1;
+    stage_k(0);
+    stage_v(0);
+    stage_v(1);
+    stage_k(1);
+    stage_k(2);
+    lds_dma::wait_vmem<4 * kLoads>();
+    lds_dma::lds_barrier();
+    scores(kB0, s0);
+    mx = largest(s0);
+    // the blocks that all queries of the workgroup see whole
+    const int whole = r0 / 32;
+    for (int u = 0; u < whole; u += 4) {
+      turn(u);
+      step(kB0, s0, s1);
+      step(kB1, s1, s0);
+      turn(u + 2);
+      step(kB2, s0, s1);
+      step(kB3, s1, s0);
     }
+    // the diagonal: a wave sees as many of its blocks as waves come before
+    // it, and a part of one more
+    auto diagonal = [&](auto block, f32x16& s, f32x16& next) __attribute__((always_inline)) {
+      if (block < wave) {
+        step(block, s, next);
+      } else if (block == wave) {
+        hide(s);
+        mx = largest(s);
+        follow();
+        bf16x8 pf[2];
+        weights(s, pf);
+        add_values(block, pf);
+      }
+    };
+    auto diagonal_tile = [&](auto block, auto block1) __attribute__((always_inline)) {
+      turn(whole + block);
+      uint8_t* vs = lds + (4 + block) * kBlockBytes;
+      bool odd = false;
+#pragma unroll
+      for (int i = 0; i < 2 * kLoads; ++i)
+        odd |= any_odd(*reinterpret_cast<const u32x4*>(vs + (i * kThreads + tid) * 16));
+      if (odd) odd_tile = block + 1;
+      lds_dma::lds_barrier();
+      odd = odd_tile == block + 1;
+      if (odd) {
+        for (int x = tid; x < kKeys * D; x += kThreads) {
+          uint16_t* w = reinterpret_cast<uint16_t*>(vs) + x;
+          if ((*w & 0x7F80u) == 0x7F80u) *w = 0;
+        }
+        lds_dma::lds_barrier();
+      }
+      diagonal(block, s0, s1);
+      diagonal(block1, s1, s0);
+      if (odd && query < len) add_odd(r0 + block * 32);
+    };
+    diagonal_tile(kB0, kB1);
+    if (keys > r0 + kKeys) diagonal_tile(kB2, kB3);
     l = xor_add(l, 32);
   }
   if (query >= len) return;
