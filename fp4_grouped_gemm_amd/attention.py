@@ -10,8 +10,8 @@ after positions, lengths, page tables or their contents change.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import struct
 
 import torch
 
@@ -19,20 +19,16 @@ from . import _check, load_library
 
 KV_BF16, KV_E4M3 = 0, 1  # FGG_KV_*
 
-
-class _KvCache(ctypes.Structure):
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
-                ("table_stride", ctypes.c_longlong), ("k_strides", ctypes.c_longlong * 3),
-                ("v_strides", ctypes.c_longlong * 3), ("dtype", ctypes.c_int),
-                ("num_pages", ctypes.c_int), ("kv_heads", ctypes.c_int),
-                ("page_size", ctypes.c_int), ("head_dim", ctypes.c_int), ("batch", ctypes.c_int),
-                ("table_width", ctypes.c_int)]
-
-
-_Strides6 = ctypes.c_longlong * 6
+# fgg_kv_cache and the strides arrays, packed with the struct module: a call on
+# one token takes about 3 us on the GPU, and filling a ctypes structure field by
+# field would cost the host as much.
+_KV_CACHE = struct.Struct("@PPPPPqqqqqqqiiiiiii")
+_STRIDES = struct.Struct("@6q")
 _CODES = (torch.float8_e4m3fn, torch.uint8)
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_raw_stream = torch._C._cuda_getCurrentRawStream
 _LIB = None
+_WORKSPACE = {}  # bytes by device and sizes
 
 
 def _lib():
@@ -40,12 +36,12 @@ def _lib():
     if _LIB is None:
         lib = load_library()
         P, I, L, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
-        C, S = ctypes.POINTER(_KvCache), ctypes.POINTER(ctypes.c_longlong)
+        B = ctypes.c_char_p  # packed structures and arrays
         for name, args in (
-            ("rope_kv_append", [C, P, P, P, S, P, I, I, I, P, P, P, P, I, I, P]),
-            ("paged_decode_attention_workspace", [C, I, ctypes.POINTER(ctypes.c_size_t)]),
-            ("paged_decode_attention", [C, P, L, L, P, F, P, I, P, ctypes.c_size_t, P]),
-            ("prompt_attention", [P, P, P, S, P, F, P, I, I, I, I, I, P]),
+            ("rope_kv_append", [B, P, P, P, B, P, I, I, I, P, P, P, P, I, I, P]),
+            ("paged_decode_attention_workspace", [B, I, ctypes.POINTER(ctypes.c_size_t)]),
+            ("paged_decode_attention", [B, P, L, L, P, F, P, I, P, ctypes.c_size_t, P]),
+            ("prompt_attention", [P, P, P, B, P, F, P, I, I, I, I, I, P]),
         ):
             fn = getattr(lib, name)
             fn.restype = ctypes.c_int
@@ -55,24 +51,28 @@ def _lib():
 
 
 def _gpu(t, name, dtype, dim, device=None):
+    """Checks a GPU tensor; returns the index of its device."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != dim:
         raise ValueError(f"{name} must be a {dim}-D {dtype} tensor")
-    if not t.is_cuda:
+    d = t.get_device()
+    if d < 0 or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return t
+    if device is not None and d != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+    return d
 
 
 def _heads(t, name, device=None):
-    """A BF16 [rows, heads, head_dim] operand; head_dim contiguous."""
-    _gpu(t, name, torch.bfloat16, 3, device)
-    if t.stride(2) != 1:
+    """A BF16 [rows, heads, head_dim] operand, head_dim contiguous: its device
+    and its strides."""
+    d = _gpu(t, name, _BF16, 3, device)
+    st = t.stride()
+    if st[2] != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    return t
+    return d, st
 
 
-def _vector(t, name, n, device, dtype=torch.int32):
+def _vector(t, name, n, device, dtype=_I32):
     _gpu(t, name, dtype, 1, device)
     if t.shape[0] != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape ({n},)")
@@ -80,53 +80,55 @@ def _vector(t, name, n, device, dtype=torch.int32):
 
 
 def _cache(k_cache, v_cache, page_table, k_scale, v_scale, device):
+    """Checks a cache: the packed fgg_kv_cache and its (pages, kv_heads,
+    page_size, head_dim), batch and table width."""
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         if not isinstance(t, torch.Tensor) or t.dim() != 4:
             raise ValueError(f"{name} must be a tensor [pages, kv_heads, page_size, head_dim]")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if k_cache.dtype != v_cache.dtype or k_cache.shape != v_cache.shape:
+        if t.get_device() != device or not t.is_cuda:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+    shape, dtype = k_cache.shape, k_cache.dtype
+    if dtype != v_cache.dtype or shape != v_cache.shape:
         raise ValueError("k_cache and v_cache must have one dtype and shape")
-    fp8 = k_cache.dtype in _CODES
-    if not fp8 and k_cache.dtype != torch.bfloat16:
-        raise ValueError(f"a cache holds bfloat16 or E4M3 codes (float8_e4m3fn / uint8), got {k_cache.dtype}")
+    fp8 = dtype in _CODES
+    if not fp8 and dtype != _BF16:
+        raise ValueError(f"a cache holds bfloat16 or E4M3 codes (float8_e4m3fn / uint8), got {dtype}")
     ks, vs = k_cache.stride(), v_cache.stride()
     if ks[3] != 1 or vs[3] != 1:
         raise ValueError("k_cache and v_cache must be contiguous in their last dimension")
-    pages, heads, page_size, dim = k_cache.shape
-    _gpu(page_table, "page_table", torch.int32, 2, device)
-    if page_table.stride(1) != 1 and page_table.shape[1] != 1:
+    pages, heads, page_size, dim = shape
+    _gpu(page_table, "page_table", _I32, 2, device)
+    batch, width = page_table.shape
+    ts = page_table.stride()
+    if ts[1] != 1 and width != 1:
         raise ValueError("page_table must be contiguous in its last dimension")
-    scales = []
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if t is not None and not fp8:
-            raise ValueError(f"{name} goes with an E4M3 cache")
-        scales.append(None if t is None else _vector(t, name, heads, device, torch.float32))
-    return _KvCache(k_cache.data_ptr(), v_cache.data_ptr(), scales[0], scales[1],
-                    page_table.data_ptr(), page_table.stride(0), ks[:3], vs[:3],
-                    KV_E4M3 if fp8 else KV_BF16, pages, heads, page_size, dim,
-                    page_table.shape[0], page_table.shape[1])
+    if not fp8 and (k_scale is not None or v_scale is not None):
+        raise ValueError("k_scale and v_scale go with an E4M3 cache")
+    k_sc = 0 if k_scale is None else _vector(k_scale, "k_scale", heads, device, _F32)
+    v_sc = 0 if v_scale is None else _vector(v_scale, "v_scale", heads, device, _F32)
+    packed = _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_sc, v_sc,
+                            page_table.data_ptr(), ts[0], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
+                            KV_E4M3 if fp8 else KV_BF16, pages, heads, page_size, dim, batch, width)
+    return packed, heads, page_size, dim, batch, width
 
 
-@contextlib.contextmanager
-def _launch(device, stream):
-    """The device of the call current; `stream` too if one is given, so that
-    memory allocated for the call belongs to the stream that uses it.  Gives the
-    raw stream."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
-        else:
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+def _elsewhere(device, stream):
+    """None if the call's device and stream are the current ones; else a context
+    that makes them so, so that memory allocated for the call belongs to the
+    stream that uses it."""
+    if stream is None:
+        return None if torch.cuda.current_device() == device else torch.cuda.device(device)
+    if stream.device.index != device:
+        raise ValueError(f"stream is on {stream.device}, expected cuda:{device}")
+    return torch.cuda.stream(stream)
 
 
-def _result(out, shape, name, device):
+def _result(out, q, shape, device):
     if out is None:
-        return torch.empty(shape, dtype=torch.bfloat16, device=device)
-    if out.dtype != torch.bfloat16 or tuple(out.shape) != tuple(shape) or out.device != device \
+        return q.new_empty(shape)
+    if out.dtype != _BF16 or tuple(out.shape) != shape or out.get_device() != device \
             or not out.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous bfloat16 tensor of shape {tuple(shape)} on {device}")
+        raise ValueError(f"out must be a contiguous bfloat16 tensor of shape {shape} on cuda:{device}")
     return out
 
 
@@ -148,30 +150,33 @@ def rope_kv_append(q, k, v, cos_sin, positions, page_table, k_cache, v_cache, *,
     Returns the rotated queries [T, Hq, D] (into `out` if given), or with
     return_k (rotated queries, rotated keys): what prompt_attention reads.
     See include/fgg.h for the exact definition."""
-    dev = _heads(q, "q").device
-    _heads(k, "k", dev)
-    _heads(v, "v", dev)
-    cache = _cache(k_cache, v_cache, page_table, k_scale, v_scale, dev)
+    dev, qs = _heads(q, "q")
+    ks, vs = _heads(k, "k", dev)[1], _heads(v, "v", dev)[1]
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return rope_kv_append(q, k, v, cos_sin, positions, page_table, k_cache, v_cache,
+                                  seq_ids=seq_ids, interleaved=interleaved, k_scale=k_scale,
+                                  v_scale=v_scale, return_k=return_k, out=out)
+    cache, hk, _, dim, _, _ = _cache(k_cache, v_cache, page_table, k_scale, v_scale, dev)
     T, hq, d = q.shape
-    hk = cache.kv_heads
-    if d != cache.head_dim or tuple(k.shape) != (T, hk, d) or tuple(v.shape) != (T, hk, d):
-        raise ValueError(f"q must be [T, Hq, {cache.head_dim}], k and v [T, {hk}, {cache.head_dim}] as the cache")
-    _gpu(cos_sin, "cos_sin", torch.float32, 2, dev)
+    if d != dim or k.shape != (T, hk, d) or v.shape != (T, hk, d):
+        raise ValueError(f"q must be [T, Hq, {dim}], k and v [T, {hk}, {dim}] as the cache")
+    _gpu(cos_sin, "cos_sin", _F32, 2, dev)
     if not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be contiguous")
+    turns, rot = cos_sin.shape
     pos = _vector(positions, "positions", T, dev)
     ids = None if seq_ids is None else _vector(seq_ids, "seq_ids", T, dev)
-    strides = _Strides6(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2])
-    with _launch(dev, stream) as s:
-        q_out = _result(out, (T, hq, d), "out", dev)
-        k_out = torch.empty((T, hk, d), dtype=torch.bfloat16, device=dev) if return_k else None
-        if T == 0:
-            return (q_out, k_out) if return_k else q_out
+    res = _result(out, q, (T, hq, d), dev)
+    k_out = q.new_empty((T, hk, d)) if return_k else None
+    if T:
+        strides = _STRIDES.pack(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1])
         _check(_lib().rope_kv_append(
-            cache, q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, cos_sin.data_ptr(),
-            cos_sin.shape[0], cos_sin.shape[1], bool(interleaved), pos, ids, q_out.data_ptr(),
-            k_out.data_ptr() if return_k else None, T, hq, s))
-    return (q_out, k_out) if return_k else q_out
+            cache, q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, cos_sin.data_ptr(), turns, rot,
+            1 if interleaved else 0, pos, ids, res.data_ptr(),
+            k_out.data_ptr() if return_k else None, T, hq, _raw_stream(dev)))
+    return (res, k_out) if return_k else res
 
 
 def paged_decode_attention(q, k_cache, v_cache, page_table, lengths, *, scale=None, k_scale=None,
@@ -182,23 +187,31 @@ def paged_decode_attention(q, k_cache, v_cache, page_table, lengths, *, scale=No
     its heads; page_table: int32 [B, W]; lengths: int32 [B], the cached tokens
     of each sequence (the new one among them); 0 gives zeros.  scale: of the
     scores, D ** -0.5 if None.  Returns bfloat16 [B, Hq, D]."""
-    dev = _heads(q, "q").device
-    cache = _cache(k_cache, v_cache, page_table, k_scale, v_scale, dev)
+    dev, qs = _heads(q, "q")
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return paged_decode_attention(q, k_cache, v_cache, page_table, lengths, scale=scale,
+                                          k_scale=k_scale, v_scale=v_scale, out=out)
+    cache, hk, page_size, dim, batch, width = _cache(k_cache, v_cache, page_table, k_scale, v_scale, dev)
     B, hq, d = q.shape
-    if d != cache.head_dim or B != cache.batch:
-        raise ValueError(f"q must be [{cache.batch}, Hq, {cache.head_dim}] as the page table and the cache")
+    if d != dim or B != batch:
+        raise ValueError(f"q must be [{batch}, Hq, {dim}] as the page table and the cache")
     lens = _vector(lengths, "lengths", B, dev)
-    scale = d ** -0.5 if scale is None else float(scale)
-    lib = _lib()
-    with _launch(dev, stream) as s:
-        res = _result(out, (B, hq, d), "out", dev)
-        if B == 0:
-            return res
-        n = ctypes.c_size_t()
-        _check(lib.paged_decode_attention_workspace(cache, hq, ctypes.byref(n)))
-        work = torch.empty(n.value, dtype=torch.uint8, device=dev)
-        _check(lib.paged_decode_attention(cache, q.data_ptr(), q.stride(0), q.stride(1), lens, scale,
-                                          res.data_ptr(), hq, work.data_ptr(), n.value, s))
+    res = _result(out, q, (B, hq, d), dev)
+    if B:
+        lib, sizes = _lib(), (dev, B, hq, hk, d, page_size * width)
+        n = _WORKSPACE.get(sizes)
+        if n is None:
+            need = ctypes.c_size_t()
+            _check(lib.paged_decode_attention_workspace(cache, hq, ctypes.byref(need)))
+            if len(_WORKSPACE) >= 4096:
+                _WORKSPACE.clear()
+            n = _WORKSPACE[sizes] = need.value
+        work = torch.empty(n, dtype=torch.uint8, device=q.device)
+        _check(lib.paged_decode_attention(cache, q.data_ptr(), qs[0], qs[1], lens,
+                                          d ** -0.5 if scale is None else float(scale),
+                                          res.data_ptr(), hq, work.data_ptr(), n, _raw_stream(dev)))
     return res
 
 
@@ -210,23 +223,24 @@ def prompt_attention(q, k, v, starts, *, scale=None, out=None, stream=None):
     non-decreasing: prompt i is the tokens [starts[i], starts[i + 1]); tokens
     of no prompt give zeros.  scale: of the scores, D ** -0.5 if None.
     Returns bfloat16 [T, Hq, D]."""
-    dev = _heads(q, "q").device
-    _heads(k, "k", dev)
-    _heads(v, "v", dev)
+    dev, qs = _heads(q, "q")
+    ks, vs = _heads(k, "k", dev)[1], _heads(v, "v", dev)[1]
+    elsewhere = _elsewhere(dev, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return prompt_attention(q, k, v, starts, scale=scale, out=out)
     T, hq, d = q.shape
     hk = k.shape[1]
-    if tuple(k.shape) != (T, hk, d) or tuple(v.shape) != (T, hk, d):
+    if k.shape != (T, hk, d) or v.shape != (T, hk, d):
         raise ValueError(f"k and v must be [{T}, Hkv, {d}] as q")
-    _gpu(starts, "starts", torch.int32, 1, dev)
-    if starts.shape[0] < 2 or not starts.is_contiguous():
+    _gpu(starts, "starts", _I32, 1, dev)
+    batch = starts.shape[0] - 1
+    if batch < 1 or not starts.is_contiguous():
         raise ValueError("starts must be a contiguous int32 tensor of shape (B + 1,), B >= 1")
-    scale = d ** -0.5 if scale is None else float(scale)
-    strides = _Strides6(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2])
-    with _launch(dev, stream) as s:
-        res = _result(out, (T, hq, d), "out", dev)
-        if T == 0:
-            return res
+    res = _result(out, q, (T, hq, d), dev)
+    if T:
+        strides = _STRIDES.pack(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1])
         _check(_lib().prompt_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), strides,
-                                       starts.data_ptr(), scale, res.data_ptr(), T,
-                                       starts.shape[0] - 1, hq, hk, d, s))
+                                       starts.data_ptr(), d ** -0.5 if scale is None else float(scale),
+                                       res.data_ptr(), T, batch, hq, hk, d, _raw_stream(dev)))
     return res

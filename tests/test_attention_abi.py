@@ -7,7 +7,7 @@ import pytest
 import fp4_grouped_gemm_amd as fgg
 
 torch = pytest.importorskip("torch")
-from fp4_grouped_gemm_amd.attention import _KvCache, _lib, _Strides6  # noqa: E402
+from fp4_grouped_gemm_amd.attention import _KV_CACHE, _lib, _STRIDES  # noqa: E402
 
 P = 0x10000  # 16-byte aligned and never dereferenced: every call below is refused
 
@@ -17,8 +17,10 @@ def _cache(**kw):
              k_strides=(4096, 1024, 128), v_strides=(4096, 1024, 128), dtype=0, num_pages=10, kv_heads=4,
              page_size=8, head_dim=128, batch=3, table_width=8)
     f.update(kw)
-    f["k_strides"], f["v_strides"] = ((ctypes.c_longlong * 3)(*f[n]) for n in ("k_strides", "v_strides"))
-    return _KvCache(*[f[n] for n, _ in _KvCache._fields_])
+    return _KV_CACHE.pack(*(f[n] or 0 for n in ("k", "v", "k_scale", "v_scale", "page_table", "table_stride")),
+                          *f["k_strides"], *f["v_strides"],
+                          *(f[n] for n in ("dtype", "num_pages", "kv_heads", "page_size", "head_dim", "batch",
+                                           "table_width")))
 
 
 CACHE = [
@@ -48,7 +50,7 @@ CACHE = [
 def _append(cache=None, q=P, k=P, v=P, strides=(1024, 128, 512, 128, 512, 128), turns=P, num=100, rot=128,
             pos=P, ids=P, q_out=P, k_out=None, T=3, q_heads=8):
     lib = _lib()
-    st = lib.rope_kv_append(cache or _cache(), q, k, v, _Strides6(*strides), turns, num, rot, 0, pos, ids,
+    st = lib.rope_kv_append(cache or _cache(), q, k, v, _STRIDES.pack(*strides), turns, num, rot, 0, pos, ids,
                             q_out, k_out, T, q_heads, None)
     return st, lib.fgg_last_error().decode()
 
@@ -62,7 +64,7 @@ def _decode(cache=None, q=P, qs=1024, qh=128, lens=P, scale=0.1, out=P, q_heads=
 def _prompt(q=P, k=P, v=P, strides=(1024, 128, 512, 128, 512, 128), starts=P, scale=0.1, out=P, T=5,
             batch=2, hq=8, hk=4, d=128):
     lib = _lib()
-    st = lib.prompt_attention(q, k, v, _Strides6(*strides), starts, scale, out, T, batch, hq, hk, d, None)
+    st = lib.prompt_attention(q, k, v, _STRIDES.pack(*strides), starts, scale, out, T, batch, hq, hk, d, None)
     return st, lib.fgg_last_error().decode()
 
 
