@@ -928,6 +928,7 @@ fgg_status paged_decode_attention(const fgg_kv_cache* cache, const void* q, long
   a.out = static_cast<uint16_t*>(out);
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = a.part_o + (size_t)workgroups * 2 * 16 * cache->head_dim;
+  a.split = reinterpret_cast<decltype(a.split)>(a.part_ml + (size_t)workgroups * 2 * 16 * 2);
   a.scale = scale;
   a.q_heads = q_heads;
   a.D = cache->head_dim;

@@ -40,6 +40,16 @@ struct AppendArgs {
   bool interleaved;
 };
 
+namespace decode_detail {
+// A row that the slices of several workgroups share, for the join; written
+// by the workgroup whose slice it begins in.
+struct SplitRow {
+  int first, last;  // those workgroups; first < 0: no such row
+  int b, head0, heads, pad[3];
+};
+static_assert(sizeof(SplitRow) == 32, "two 16-byte loads");
+}  // namespace decode_detail
+
 struct DecodeArgs {
   KvCache c;
   const uint16_t* q;
@@ -48,6 +58,7 @@ struct DecodeArgs {
   uint16_t* out;  // [batch, q_heads, D]
   float* part_o;  // [workgroups, 2, 16, D] unnormalised outputs of split rows
   float* part_ml; // [workgroups, 2, 16, 2] their maxima (log2 domain) and sums
+  decode_detail::SplitRow* split;  // [workgroups] rows to join
   float scale;
   int q_heads, D;
 };
@@ -65,7 +76,7 @@ struct PromptArgs {
 
 // Workgroups of a decode launch, from the longest length the table can hold.
 int decode_workgroups(int batch, int q_heads, int kv_heads, long long max_len, int num_cus);
-// Bytes of its workspace (part_o and part_ml) for that many workgroups.
+// Bytes of its workspace (part_o, part_ml, split) for that many workgroups.
 size_t decode_workspace(int workgroups, int D);
 
 hipError_t launch_append(const AppendArgs& a, hipStream_t s);

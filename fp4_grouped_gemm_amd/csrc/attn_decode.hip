@@ -35,9 +35,7 @@ constexpr int kWaveTokens = 32;
 constexpr int kTile = kWaves * kWaveTokens;
 constexpr int kMaxHeads = 16;  // query heads of a KV head in one row of work
 
-struct Plan {
-  int total, per;  // tiles of the batch, and of a workgroup
-};
+constexpr int kPerCu = 3;  // workgroups on a compute unit: as many as their registers allow
 
 __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
   const long long cap = (long long)a.c.width << a.c.page_shift;
@@ -47,26 +45,20 @@ __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
 // An empty row has a tile too: the one that writes its zeros.
 __device__ __forceinline__ int tiles_of(int len) { return len ? (len + kTile - 1) / kTile : 1; }
 
-// Row of values d0.. of the group's rows of work of a KV head.
+// Rows of work of a KV head: its query heads by kMaxHeads.
 __device__ __forceinline__ int head_groups(const DecodeArgs& a) {
   return (a.q_heads / a.c.kv_heads + kMaxHeads - 1) / kMaxHeads;
 }
 
-// Tiles before sequence b in one head row, for the sequence that holds tile
-// `pos` of the list (rows = heads of work per sequence).  All threads call.
-struct Place {
-  int b, before;
-};
-__device__ __forceinline__ int scan_lengths(const DecodeArgs& a, int* lds, int& base) {
-  const int per = (a.c.batch + kThreads - 1) / kThreads;
-  const int b0 = threadIdx.x * per, b1 = min(b0 + per, a.c.batch);
-  int sum = 0;
-  for (int b = b0; b < b1; ++b) sum += tiles_of(length_of(a, b));
-  return block_scan<kThreads>(sum, base, lds);
+// The join has a place for each row of the batch if there are no more rows
+// than slices, else one for each slice (a slice holds the beginning of one
+// shared row at most).
+__device__ __host__ __forceinline__ bool joins_by_row(int rows, int workgroups) {
+  return rows <= workgroups;
 }
 
 template <int D, bool FP8>
-__global__ __launch_bounds__(kThreads, 2) void decode_kernel(DecodeArgs a) {
+__global__ __launch_bounds__(kThreads, kPerCu) void decode_kernel(DecodeArgs a) {
   constexpr int kSteps = D / 32;                // k-steps of a QK product
   constexpr int kBlocks = D / 16;               // 16-row blocks of O^T
   constexpr int kRow = D * 2 + 32;              // LDS bytes of a staged V row (BF16)
@@ -78,8 +70,6 @@ __global__ __launch_bounds__(kThreads, 2) void decode_kernel(DecodeArgs a) {
   constexpr int kJoinBytes = kWaves * kMaxHeads * kOutRow * 4;
   __shared__ __align__(16) uint8_t stage[kStageBytes > kJoinBytes ? kStageBytes : kJoinBytes];
   __shared__ float ml[kWaves][kMaxHeads][2];
-  __shared__ int scan_lds[kWaves];
-  __shared__ int start_b, start_before;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -88,29 +78,36 @@ __global__ __launch_bounds__(kThreads, 2) void decode_kernel(DecodeArgs a) {
   const int group_heads = a.q_heads / a.c.kv_heads;
   const int rows = a.c.kv_heads * groups;  // rows of work of a sequence
 
-  // this workgroup's slice of the list
-  int base;
-  const int seq_tiles = scan_lengths(a, scan_lds, base);
-  const int total = seq_tiles * rows;
-  const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
-  int pos = (int)blockIdx.x * per;
-  const int end = min(total, pos + per);
-  if (pos >= end) return;
+  // This workgroup's slice of the list, and the sequence that it begins in.
+  // Each wave goes over the lengths by itself, some to a lane.
+  int b, before, total;  // `before`: tiles of one row of each earlier sequence
   {
-    const int chunk = (a.c.batch + kThreads - 1) / kThreads;
-    const int b1 = min((tid + 1) * chunk, a.c.batch);
-    int before = base;
-    for (int b = tid * chunk; b < b1; ++b) {
+    const int chunk = (a.c.batch + 63) / 64;
+    const int b0 = lane * chunk, b1 = min(b0 + chunk, a.c.batch);
+    int sum = 0;
+    for (int i = b0; i < b1; ++i) sum += tiles_of(length_of(a, i));
+    int upto = sum;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int u = __shfl_up(upto, off, 64);
+      if (lane >= off) upto += u;
+    }
+    total = __builtin_amdgcn_readlane(upto, 63) * rows;
+    const int first = min((int)blockIdx.x * ((total + (int)gridDim.x - 1) / (int)gridDim.x), total - 1);
+    // the lane whose sequences hold tile `first`, then the sequence
+    const int src = __builtin_ctzll(__ballot(first < upto * rows));
+    before = __builtin_amdgcn_readlane(upto - sum, src);
+    for (b = src * chunk;; ++b) {
       const int n = tiles_of(length_of(a, b));
-      if (before * rows <= pos && pos < (before + n) * rows) {
-        start_b = b;
-        start_before = before;
-      }
+      if (first < (before + n) * rows) break;
       before += n;
     }
   }
-  __syncthreads();
-  int b = start_b, before = start_before;
+  const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+  int pos = (int)blockIdx.x * per;
+  const int end = min(total, pos + per);
+  const bool by_row = joins_by_row(a.c.batch * rows, (int)gridDim.x);
+  if (!by_row && tid == 0) a.split[blockIdx.x].first = -1;
 
   uint8_t* const my_stage = stage + wave * (kWaveTokens * kRow);
   while (pos < end) {
@@ -259,6 +256,13 @@ __global__ __launch_bounds__(kThreads, 2) void decode_kernel(DecodeArgs a) {
     }
     __syncthreads();
     const bool whole = t0 == 0 && t1 == n;
+    if (t0 == 0 && tid == 0) {
+      if (!whole)
+        a.split[by_row ? b * rows + row : (int)blockIdx.x] =
+            SplitRow{(int)blockIdx.x, (int)blockIdx.x + (n - t1 + per - 1) / per, b, head0, heads, {}};
+      else if (by_row)
+        a.split[b * rows + row].first = -1;
+    }
     const int piece = (int)blockIdx.x * 2 + (t0 > 0 ? 0 : 1);
     {
       constexpr int kPer = D * kMaxHeads / kThreads;  // outputs of a thread: 8 or 4
@@ -309,75 +313,78 @@ __global__ __launch_bounds__(kThreads, 2) void decode_kernel(DecodeArgs a) {
 }
 
 // Joins the pieces of the rows that the slices of several workgroups share.
-// One workgroup per query head and sequence; the pieces go to groups of D / 4
-// lanes in turn.
+// Workgroup (x, y) takes heads 2 y and 2 y + 1 of the row in place x, if there
+// is one.  The pieces of a head go to groups of
+// D / 4 lanes in turn, kAhead of them loaded at once: a row over all slices
+// (128 pieces) takes two round trips to memory.
+constexpr int kJoinThreads = 512;
+constexpr int kAhead = 8;
+
 template <int D>
-__global__ __launch_bounds__(kThreads) void join_kernel(DecodeArgs a, int workgroups) {
-  constexpr int kLanes = D / 4, kSets = kThreads / kLanes;
-  __shared__ int scan_lds[kWaves];
-  __shared__ int my_before;
-  __shared__ float red_m[kWaves];
-  __shared__ __align__(16) float red_o[kSets][D];
-  __shared__ float red_l[kSets];
-  const int tid = threadIdx.x;
-  const int b = (int)blockIdx.x / a.q_heads, h = (int)blockIdx.x % a.q_heads;
-  const int group_heads = a.q_heads / a.c.kv_heads, groups = head_groups(a);
-  const int rows = a.c.kv_heads * groups;
-  const int n = tiles_of(length_of(a, b));
-  if (n == 1) return;
-  int base;
-  const int total = scan_lengths(a, scan_lds, base) * rows;
-  {
-    const int chunk = (a.c.batch + kThreads - 1) / kThreads;
-    if (b >= tid * chunk && b < (tid + 1) * chunk) {
-      int before = base;
-      for (int i = tid * chunk; i < b; ++i) before += tiles_of(length_of(a, i));
-      my_before = before;
-    }
-  }
-  __syncthreads();
-  const int per = (total + workgroups - 1) / workgroups;
-  const int kvh = h / group_heads, hh = h - kvh * group_heads;
-  const int s0 = my_before * rows + (kvh * groups + hh / kMaxHeads) * n, s1 = s0 + n;
-  const int first = s0 / per, last = (s1 - 1) / per;
-  if (first == last) return;  // one workgroup had the whole row
-  const int hr = hh % kMaxHeads;
-  // piece of workgroup w: slot 0 if the row began before its slice
-  auto piece_of = [&](int w) { return (w * 2 + (s0 < w * per ? 0 : 1)) * kMaxHeads + hr; };
-  float m = kNegInf;
-  for (int w = first + tid; w <= last; w += kThreads) m = fmaxf(m, a.part_ml[piece_of(w) * 2]);
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) m = xor_max(m, off);
-  if ((tid & 63) == 0) red_m[tid >> 6] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) m = fmaxf(m, red_m[w]);
-  const float ms = m == kNegInf ? 0.f : m;
-  const int set = tid / kLanes, d = (tid % kLanes) * 4;
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(DecodeArgs a) {
+  constexpr int kLanes = D / 4, kSets = kJoinThreads / 2 / kLanes;
+  __shared__ __align__(16) float red_o[2][kSets][D];
+  __shared__ float red_ml[2][kSets][2];
+  const SplitRow row = a.split[blockIdx.x];
+  const int first = row.first, last = row.last;
+  if (first < 0) return;
+  const int which = threadIdx.x / (kJoinThreads / 2), t = threadIdx.x % (kJoinThreads / 2);
+  const int h = min((int)blockIdx.y * 2 + which, kMaxHeads - 1);
+  const int set = t / kLanes, d = (t % kLanes) * 4;
+  float m = kNegInf, l = 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  float l = 0.f;
-  for (int w = first + set; w <= last; w += kSets) {
-    const int p = piece_of(w);
-    const float f = __builtin_amdgcn_exp2f(a.part_ml[p * 2] - ms);
-    l += f * a.part_ml[p * 2 + 1];
-    o += f * *reinterpret_cast<const f32x4*>(a.part_o + (long long)p * D + d);
-  }
-  *reinterpret_cast<f32x4*>(&red_o[set][d]) = o;
-  if (d == 0) red_l[set] = l;
-  __syncthreads();
-  if (tid < kLanes) {
-    float L = 0.f;
-    f32x4 r = {0.f, 0.f, 0.f, 0.f};
+  for (int w0 = first + set; w0 <= last; w0 += kSets * kAhead) {
+    f32x2 ml[kAhead];
+    f32x4 x[kAhead];
 #pragma unroll
-    for (int i = 0; i < kSets; ++i) {
-      L += red_l[i];
-      r += *reinterpret_cast<const f32x4*>(&red_o[i][tid * 4]);
+    for (int i = 0; i < kAhead; ++i) {
+      // past the last piece: the last one again, without weight
+      const int w = min(w0 + i * kSets, last);
+      const int p = (w * 2 + (w == first ? 1 : 0)) * kMaxHeads + h;
+      ml[i] = *reinterpret_cast<const f32x2*>(a.part_ml + p * 2);
+      x[i] = *reinterpret_cast<const f32x4*>(a.part_o + (long long)p * D + d);
     }
-    const float vs = a.c.fp8 && a.c.v_scale ? a.c.v_scale[kvh] : 1.0f;
-    r *= L == 0.f ? 0.f : vs / L;
-    *reinterpret_cast<uint2*>(a.out + ((long long)b * a.q_heads + h) * D + tid * 4) =
-        pack_bf16x4(r[0], r[1], r[2], r[3]);
+    float m1 = m;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) m1 = fmaxf(m1, ml[i][0]);
+    const float ms = m1 == kNegInf ? 0.f : m1;
+    const float alpha = __builtin_amdgcn_exp2f(m - ms);
+    m = m1;
+    l *= alpha;
+    o *= alpha;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (w0 + i * kSets > last) continue;
+      const float f = __builtin_amdgcn_exp2f(ml[i][0] - ms);
+      l += f * ml[i][1];
+      o += f * x[i];
+    }
   }
+  *reinterpret_cast<f32x4*>(&red_o[which][set][d]) = o;
+  if (d == 0) {
+    red_ml[which][set][0] = m;
+    red_ml[which][set][1] = l;
+  }
+  __syncthreads();
+  if (t >= kLanes || (int)blockIdx.y * 2 + which >= row.heads) return;
+  float M = kNegInf;
+#pragma unroll
+  for (int i = 0; i < kSets; ++i) M = fmaxf(M, red_ml[which][i][0]);
+  const float ms = M == kNegInf ? 0.f : M;
+  float L = 0.f;
+  f32x4 r = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kSets; ++i) {
+    const float f = __builtin_amdgcn_exp2f(red_ml[which][i][0] - ms);
+    L += f * red_ml[which][i][1];
+    r += f * *reinterpret_cast<const f32x4*>(&red_o[which][i][d]);
+  }
+  const int head = row.head0 + h;
+  const float vs =
+      a.c.fp8 && a.c.v_scale ? a.c.v_scale[head / (a.q_heads / a.c.kv_heads)] : 1.0f;
+  r *= L == 0.f ? 0.f : vs / L;
+  *reinterpret_cast<uint2*>(a.out + ((long long)row.b * a.q_heads + head) * D + d) =
+      pack_bf16x4(r[0], r[1], r[2], r[3]);
 }
 
 template <int D>
@@ -389,8 +396,11 @@ hipError_t launch(const DecodeArgs& a, int workgroups, hipStream_t s) {
   hipError_t e = hipGetLastError();
   // a row of one tile is never split: tables that hold no more need no join
   if (e != hipSuccess || ((long long)a.c.width << a.c.page_shift) <= kTile) return e;
-  hipLaunchKernelGGL((join_kernel<D>), dim3((unsigned)(a.c.batch * a.q_heads)), dim3(kThreads), 0, s, a,
-                     workgroups);
+  const int heads = a.q_heads / a.c.kv_heads < kMaxHeads ? a.q_heads / a.c.kv_heads : kMaxHeads;
+  const long long rows = (long long)a.c.batch * a.c.kv_heads *
+                         ((a.q_heads / a.c.kv_heads + kMaxHeads - 1) / kMaxHeads);
+  const int places = joins_by_row((int)rows, workgroups) ? (int)rows : workgroups;
+  hipLaunchKernelGGL((join_kernel<D>), dim3(places, (heads + 1) / 2), dim3(kJoinThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -401,12 +411,12 @@ using namespace decode_detail;
 int decode_workgroups(int batch, int q_heads, int kv_heads, long long max_len, int num_cus) {
   const long long groups = (q_heads / kv_heads + kMaxHeads - 1) / kMaxHeads;
   const long long tiles = (long long)batch * kv_heads * groups * ((max_len + kTile - 1) / kTile);
-  const long long cap = 2LL * num_cus;
+  const long long cap = (long long)kPerCu * num_cus;
   return (int)(tiles < 1 ? 1 : tiles < cap ? tiles : cap);
 }
 
 size_t decode_workspace(int workgroups, int D) {
-  return (size_t)workgroups * 2 * kMaxHeads * (D + 2) * sizeof(float);
+  return (size_t)workgroups * (2 * kMaxHeads * (D + 2) * sizeof(float) + sizeof(SplitRow));
 }
 
 hipError_t launch_decode(const DecodeArgs& a, int workgroups, hipStream_t s) {
