@@ -17,11 +17,11 @@
 //
 // A masked value must not reach the output even where it is infinite or NaN:
 // masked scores are overwritten, but in the product with V a weight of 0
-// times such a value is NaN.  Only the tiles on the diagonal hold values that
-// some queries of the workgroup see and others do not; those are looked over
-// as they are staged, and in the rare tile that holds a value that is not
-// finite, such values are staged as zeros for the product and added by hand
-// to the queries that see them.
+// times such a value is NaN.  Only in its last block does a wave have queries
+// that do not see every key, so it looks that block's values over as it reads
+// them; in the rare one that holds a value that is not finite, such values
+// count as zeros in the product and are added by hand to the queries that
+// see them.
 #include "attn.h"
 
 #include <type_traits>
@@ -34,7 +34,6 @@ using namespace attn;
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kRows = 32 * kWaves;  // queries of a workgroup
-constexpr int kKeys = 64;           // keys of a tile
 constexpr float kSlack = 8.f;       // weights may reach 2^kSlack before a rescaling
 
 // Segment i of the packed tokens: 0 is what lies before the first prompt,
@@ -45,15 +44,16 @@ __device__ __forceinline__ void segment(const PromptArgs& a, int i, int& lo, int
   hi = i > a.batch ? a.T : min(max(a.starts[i], 0), a.T);
   if (hi < lo) hi = lo;
 }
-__device__ __forceinline__ int row_tiles(int lo, int hi) { return (hi - lo + kRows - 1) / kRows; }
+// Its tiles of `rows` queries.
+__device__ __forceinline__ int row_tiles(int lo, int hi, int rows) { return (hi - lo + rows - 1) / rows; }
 
-// Whether one of eight BF16 values is infinite or NaN.
-__device__ __forceinline__ bool any_odd(u32x4 w) {
-  bool odd = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    odd |= (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u;
-  return odd;
+// The two BF16 values of a word: bits 15 and 31 of odd_bits tell whether they
+// are infinite or NaN (an exponent of all ones plus one carries there, and no
+// further); without_odd puts zeros in their place.
+__device__ __forceinline__ uint32_t odd_bits(uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; }
+__device__ __forceinline__ uint32_t without_odd(uint32_t w) {
+  const uint32_t odd = odd_bits(w);
+  return w & ~((odd & 0x8000u ? 0xFFFFu : 0u) | (odd & 0x80000000u ? 0xFFFF0000u : 0u));
 }
 
 // LDS layout of a staged tile: row r at r D 2 bytes, its 16-byte chunk c at
@@ -68,6 +68,21 @@ __device__ __forceinline__ int k_key(int r) {
 template <int D>
 __device__ __forceinline__ int v_key(int r) {
   return D == 128 ? ((r & 3) << 2) | ((r >> 1) & 2) : ((r << 1) & 4) | ((r >> 1) & 2);
+}
+
+// A direct load into LDS as lds_dma::dma16, except that the compiler may move
+// LDS reads across it: what it overwrites is not read between two barriers.
+__device__ __forceinline__ void dma16(i32x4 rs, uint32_t lds, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff),
+               "s"(rs), "s"(soff)
+               : "m0");
+}
+
+// Moves a buffer resource's base on.
+__device__ __forceinline__ void advance(i32x4& rs, long long bytes) {
+  const uint64_t at = ((uint64_t)(uint32_t)rs[1] << 32 | (uint32_t)rs[0]) + (uint64_t)bytes;
+  rs[0] = (int)(uint32_t)at;
+  rs[1] = (int)(uint32_t)(at >> 32);
 }
 
 // Maximum over a lane and its partner in the other half of the wave.
@@ -86,9 +101,6 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
   constexpr int kLoads = kBlockBytes / 16 / kThreads;  // chunks of a block per thread
   // rings of four blocks of K and four of V: two are read while two land
   __shared__ __align__(16) uint8_t lds[8 * kBlockBytes];
-  __shared__ int scan_lds[kWaves];
-  __shared__ int my_seg, my_tile;
-  __shared__ int odd_tile;  // 1 + the diagonal tile found to hold a value that is not finite
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -99,37 +111,38 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
   const int hid = (int)blockIdx.x % a.q_heads, item = (int)blockIdx.x / a.q_heads;
   const int kvh = hid % a.kv_heads;
   const int head = kvh * (a.q_heads / a.kv_heads) + hid / a.kv_heads;
+  // Each wave goes over the segments by itself, some to a lane.
+  int seg, lo, len, tile;
   {
-    const int segs = a.batch + 2, per = (segs + kThreads - 1) / kThreads;
-    const int i0 = tid * per, i1 = min(i0 + per, segs);
-    int sum = 0, lo, hi, base;
+    const int segs = a.batch + 2, chunk = (segs + 63) / 64;
+    const int i0 = min(lane * chunk, segs), i1 = min(i0 + chunk, segs);
+    int sum = 0, hi;
     for (int i = i0; i < i1; ++i) {
       segment(a, i, lo, hi);
-      sum += row_tiles(lo, hi);
+      sum += row_tiles(lo, hi, kRows);
     }
-    if (tid == 0) {
-      my_seg = -1;
-      odd_tile = 0;
+    int upto = sum;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int x = __shfl_up(upto, off, 64);
+      if (lane >= off) upto += x;
     }
-    block_scan<kThreads>(sum, base, scan_lds);
-    for (int i = i0; i < i1; ++i) {
-      segment(a, i, lo, hi);
-      const int n = row_tiles(lo, hi);
-      if (base <= item && item < base + n) {
-        my_seg = i;
-        my_tile = n - 1 - (item - base);  // the tiles with the most keys first
-      }
-      base += n;
+    const uint64_t past = __ballot(item < upto);
+    if (past == 0) return;
+    const int src = __builtin_ctzll(past);
+    int before = __builtin_amdgcn_readlane(upto - sum, src), n;
+    for (seg = src * chunk;; ++seg) {
+      segment(a, seg, lo, hi);
+      n = row_tiles(lo, hi, kRows);
+      if (item < before + n) break;
+      before += n;
     }
+    seg = __builtin_amdgcn_readfirstlane(seg);
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    len = __builtin_amdgcn_readfirstlane(hi) - lo;
+    tile = __builtin_amdgcn_readfirstlane(n - 1 - (item - before));  // the tiles with the most keys first
   }
-  __syncthreads();
-  const int seg = __builtin_amdgcn_readfirstlane(my_seg);
-  if (seg < 0) return;
-  int lo, hi;
-  segment(a, seg, lo, hi);
-  lo = __builtin_amdgcn_readfirstlane(lo);
-  const int len = __builtin_amdgcn_readfirstlane(hi) - lo;
-  const int r0 = __builtin_amdgcn_readfirstlane(my_tile) * kRows;
+  const int r0 = tile * kRows;
   const int w0 = r0 + wave * 32;  // this wave's first query
   const int query = w0 + col;
   const bool real = seg >= 1 && seg <= a.batch;
@@ -164,41 +177,48 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
     // Staging: load i of a wave fills 64 chunks, rows of kChunks, in LDS
     // order; a lane fetches the chunk that belongs at its place.  Rows past
     // the last key are past the resource's end and read as zeros.
+    // A load moves a multiple of 16 rows, which leaves the chunk keys as they are.
     const int row_in = tid / kChunks, chunk_in = tid % kChunks;
     constexpr int kRowsPerLoad = kThreads / kChunks;
-    const uint32_t k_off = (uint32_t)(row_in * a.k_token * 2), v_off = (uint32_t)(row_in * a.v_token * 2);
+    const uint32_t k_at = (uint32_t)(row_in * a.k_token * 2) + ((chunk_in ^ k_key<D>(row_in)) << 4);
+    const uint32_t v_at = (uint32_t)(row_in * a.v_token * 2) + ((chunk_in ^ v_key<D>(row_in)) << 4);
+    const uint32_t k_load = (uint32_t)(kRowsPerLoad * 2) * (uint32_t)a.k_token;
+    const uint32_t v_load = (uint32_t)(kRowsPerLoad * 2) * (uint32_t)a.v_token;
     const uint32_t lds0 = lds_dma::lds_addr(lds) + wave * 1024;
-    auto stage = [&](const uint16_t* p, long long stride, uint32_t off, bool value, int block) __attribute__((always_inline)) {
+    auto stage = [&](const uint16_t* p, long long stride, uint32_t at, uint32_t load, int ring, int block) __attribute__((always_inline)) {
       const int left = min(keys - block * 32, 32);
       const i32x4 rs = lds_dma::rsrc(p + (long long)block * 32 * stride,
                                      left > 0 ? (uint32_t)((left - 1) * (uint32_t)stride + D) * 2 : 0u);
-      const uint32_t at = lds0 + ((value ? 4 : 0) + (block & 3)) * kBlockBytes;
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int r = row_in + i * kRowsPerLoad;
-        const int c = chunk_in ^ (value ? v_key<D>(r) : k_key<D>(r));
-        lds_dma::dma16(rs, at + i * (kThreads * 16),
-                       r < left ? off + (uint32_t)(i * kRowsPerLoad) * (uint32_t)stride * 2 + (c << 4)
-                                : lds_dma::kSkip, 0);
-      }
+      for (int i = 0; i < kLoads; ++i)
+        dma16(rs, lds0 + (ring + (block & 3)) * kBlockBytes + i * (kThreads * 16),
+              row_in + i * kRowsPerLoad < left ? at : lds_dma::kSkip, i * load);
     };
-    auto stage_k = [&](int block) __attribute__((always_inline)) { stage(kp, a.k_token, k_off, false, block); };
-    auto stage_v = [&](int block) __attribute__((always_inline)) { stage(vp, a.v_token, v_off, true, block); };
+    auto stage_k = [&](int block) __attribute__((always_inline)) { stage(kp, a.k_token, k_at, k_load, 0, block); };
+    auto stage_v = [&](int block) __attribute__((always_inline)) { stage(vp, a.v_token, v_at, v_load, 4, block); };
+    // LDS addresses of the lane's K fragments in the first block of the ring
+    typedef const __attribute__((address_space(3))) bf16x8* lds_bf16x8;
+    uint32_t k_lds[kSteps];
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      k_lds[k] = lds_dma::lds_addr(lds) + col * kRowBytes + (((2 * k + half) ^ k_key<D>(col)) << 4);
+      asm("" : "+v"(k_lds[k]));  // kept whole: a block's place is the read's constant offset
+    }
     const int v_row = half * 4 + ((lane & 15) >> 2);
 
+    const int whole = r0 / 32;  // blocks that all queries of the workgroup see whole
     // The steps of a block of 32 keys: its scores, the largest one, the
     // weights, their product with the values.  `block` (a constant) counts the
     // four blocks of the two tiles in LDS.
     float mx;
-    auto scores = [&](auto block, f32x16& s) __attribute__((always_inline)) {
-      const uint8_t* ks = lds + block * kBlockBytes;
+    auto scores = [&](auto block, f32x16& s, auto between) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < 16; ++j) s[j] = 0.f;
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
-        const bf16x8 kf = *reinterpret_cast<const bf16x8*>(
-            ks + col * kRowBytes + (((2 * k + half) ^ k_key<D>(col)) << 4));
+        const bf16x8 kf = *(lds_bf16x8)(k_lds[k] + block * kBlockBytes);
         s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[k], s, 0, 0, 0);
+        if (k & 1) between(k >> 1);
       }
     };
     // keys after the query, in the block that starts with the wave's first one
@@ -211,14 +231,17 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
       float x = s[0];
 #pragma unroll
       for (int j = 1; j < 16; ++j) x = fmaxf(x, s[j]);
-      return half_max(x);
+      return x;
     };
     // The subtrahend follows the maximum only when that would let a weight
     // pass 2^kSlack: the outputs are then scaled down, which late blocks
-    // almost never need.  A query's result depends on its own scores only.
+    // almost never need.  So a lane looks at its own keys' scores, and only
+    // then at those of the lane with the query's other keys.  A query's result
+    // depends on its own scores only.
     auto follow = [&]() __attribute__((always_inline)) {
-      const bool grown = (mx - m) * scale2 > kSlack;
-      if (__any(grown)) {
+      if (__any((mx - m) * scale2 > kSlack)) {
+        mx = half_max(mx);
+        const bool grown = (mx - m) * scale2 > kSlack;
         const float alpha = grown ? __builtin_amdgcn_exp2f((m - mx) * scale2) : 1.f;
         m = grown ? mx : m;
         l *= alpha;
@@ -244,25 +267,8 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
       }
       l += sum0 + sum1;
     };
-    auto add_values = [&](auto block, const bf16x8 (&pf)[2]) __attribute__((always_inline)) {
-      const uint8_t* vs = lds + (4 + block) * kBlockBytes;
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int i = 0; i < kBlocks; ++i) {
-          u32x2 x[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = k * 16 + e * 8 + v_row;
-            const int c = i * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-            x[e] = lds_read_tr(vs + r * kRowBytes + ((c ^ v_key<D>(r)) << 4) + (lane & 1) * 8);
-          }
-          const bf16x8 vf = __builtin_bit_cast(bf16x8, (u32x4){x[0][0], x[0][1], x[1][0], x[1][1]});
-          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[k], acc[i], 0, 0, 0);
-        }
-    };
     auto add_odd = [&](int k0) __attribute__((always_inline)) {
-      for (int u = k0; u <= min(query, k0 + kKeys - 1); ++u) {
+      for (int u = k0; u <= query; ++u) {
         const uint16_t* v = vp + (long long)u * a.v_token;
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i)
@@ -273,34 +279,100 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
           }
       }
     };
-
+    // V^T operand of 16 keys (half of a block) and 32 of its dims
+    auto value = [&](auto block, int k, int i) __attribute__((always_inline)) {
+      const uint8_t* vs = lds + (4 + block) * kBlockBytes;
+      u32x2 x[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = k * 16 + e * 8 + v_row;
+        const int c = i * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+        x[e] = lds_read_tr(vs + r * kRowBytes + ((c ^ v_key<D>(r)) << 4) + (lane & 1) * 8);
+      }
+      return (u32x4){x[0][0], x[0][1], x[1][0], x[1][1]};
+    };
+    auto add_values = [&](auto block, const bf16x8 (&pf)[2]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i)
+          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              __builtin_bit_cast(bf16x8, value(block, k, i)), pf[k], acc[i], 0, 0, 0);
+    };
+    // the same of the wave's last block
+    auto add_last_values = [&](int block, const bf16x8 (&pf)[2]) __attribute__((always_inline)) {
+      bool any = false;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        u32x4 v[kBlocks];
+        uint32_t odd = 0;
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+          v[i] = value(block, k, i);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) odd |= odd_bits(v[i][x]);
+        }
+        if (__any((odd & 0x80008000u) != 0)) {
+          any = true;
+#pragma unroll
+          for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) v[i][x] = without_odd(v[i][x]);
+        }
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i)
+          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v[i]), pf[k],
+                                                           acc[i], 0, 0, 0);
+      }
+      if (any && query < len) add_odd(w0);
+    };
     // Takes the scores of a block through softmax and values while it computes
     // those of the next one: matrix and vector work of one wave that do not
     // wait for each other.
-    auto step = [&](auto block, f32x16& s, f32x16& next) __attribute__((always_inline)) {
+    auto step = [&](auto block, f32x16& s, f32x16& next, auto between) __attribute__((always_inline)) {
       follow();
       bf16x8 pf[2];
-      scores(std::integral_constant<int, (block + 1) % 4>{}, next);
+      scores(std::integral_constant<int, (block + 1) % 4>{}, next, between);
       weights(s, pf);
       add_values(block, pf);
       mx = largest(next);
     };
-    // Landed after this: V of blocks u and u + 1, K of u + 1 and u + 2; every
-    // wave is done with the blocks before those, whose places the next ones
-    // take.
-    auto turn = [&](int u) __attribute__((always_inline)) {
+    // Landed after this at block u: V of u and u + 1, K of u + 1 and u + 2; every
+    // wave is done with the blocks before those, whose places V of u + 2 and u +
+    // 3 and K of u + 3 and u + 4 take.
+    auto turn = [&]() __attribute__((always_inline)) {
       lds_dma::wait_vmem<0>();
       lds_dma::lds_barrier();
+    };
+    auto stage_ahead = [&](int u) __attribute__((always_inline)) {
       stage_v(u + 2);
       stage_v(u + 3);
       stage_k(u + 3);
       stage_k(u + 4);
     };
+    auto nothing = [](int) {};
+    f32x16 s0, s1;
+    // Away from the last keys there is nothing to check: the bases move on by
+    // two blocks, the rows of the loads are scalar offsets, and the loads go out
+    // one at a time between matrix instructions.
+    i32x4 k_rs = lds_dma::rsrc(kp + 96 * a.k_token, 0xFFFFFFFFu);  // K of block 3, V of block 2
+    i32x4 v_rs = lds_dma::rsrc(vp + 64 * a.v_token, 0xFFFFFFFFu);
+    auto two_steps = [&](auto block) __attribute__((always_inline)) {
+      turn();
+      step(block, s0, s1, [&](int i) __attribute__((always_inline)) {
+        dma16(v_rs, lds0 + (4 + (block + 2) % 4) * kBlockBytes + i * (kThreads * 16), v_at, i * v_load);
+      });
+      step(std::integral_constant<int, block + 1>{}, s1, s0, [&](int i) __attribute__((always_inline)) {
+        dma16(k_rs, lds0 + (block + 3 + i / kLoads) % 4 * kBlockBytes + i % kLoads * (kThreads * 16),
+              k_at, i * k_load);
+      });
+      advance(k_rs, 128 * a.k_token);
+      advance(v_rs, 128 * a.v_token);
+    };
     constexpr std::integral_constant<int, 0> kB0;
     constexpr std::integral_constant<int, 1> kB1;
     constexpr std::integral_constant<int, 2> kB2;
     constexpr std::integral_constant<int, 3> kB3;
-    f32x16 s0, s1;
     stage_k(0);
     stage_v(0);
     stage_v(1);
@@ -308,55 +380,38 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
     stage_k(2);
     lds_dma::wait_vmem<4 * kLoads>();
     lds_dma::lds_barrier();
-    scores(kB0, s0);
+    scores(kB0, s0, nothing);
     mx = largest(s0);
-    // the blocks that all queries of the workgroup see whole
-    const int whole = r0 / 32;
-    for (int u = 0; u < whole; u += 4) {
-      turn(u);
-      step(kB0, s0, s1);
-      step(kB1, s1, s0);
-      turn(u + 2);
-      step(kB2, s0, s1);
-      step(kB3, s1, s0);
+    for (int u = 0; u + 4 < whole; u += 4) {
+      two_steps(kB0);
+      two_steps(kB2);
     }
-    // the diagonal: a wave sees as many of its blocks as waves come before
-    // it, and a part of one more
-    auto diagonal = [&](auto block, f32x16& s, f32x16& next) __attribute__((always_inline)) {
-      if (block < wave) {
-        step(block, s, next);
-      } else if (block == wave) {
-        hide(s);
-        mx = largest(s);
-        follow();
-        bf16x8 pf[2];
-        weights(s, pf);
-        add_values(block, pf);
-      }
-    };
-    auto diagonal_tile = [&](auto block, auto block1) __attribute__((always_inline)) {
-      turn(whole + block);
-      uint8_t* vs = lds + (4 + block) * kBlockBytes;
-      bool odd = false;
-#pragma unroll
-      for (int i = 0; i < 2 * kLoads; ++i)
-        odd |= any_odd(*reinterpret_cast<const u32x4*>(vs + (i * kThreads + tid) * 16));
-      if (odd) odd_tile = block + 1;
-      lds_dma::lds_barrier();
-      odd = odd_tile == block + 1;
-      if (odd) {
-        for (int x = tid; x < kKeys * D; x += kThreads) {
-          uint16_t* w = reinterpret_cast<uint16_t*>(vs) + x;
-          if ((*w & 0x7F80u) == 0x7F80u) *w = 0;
-        }
-        lds_dma::lds_barrier();
-      }
-      diagonal(block, s0, s1);
-      diagonal(block1, s1, s0);
-      if (odd && query < len) add_odd(r0 + block * 32);
-    };
-    diagonal_tile(kB0, kB1);
-    if (keys > r0 + kKeys) diagonal_tile(kB2, kB3);
+    if (whole) {
+      turn();
+      stage_ahead(whole - 4);
+      step(kB0, s0, s1, nothing);
+      step(kB1, s1, s0, nothing);
+      turn();
+      stage_ahead(whole - 2);
+      step(kB2, s0, s1, nothing);
+      step(kB3, s1, s0, nothing);
+    }
+    // the diagonal: a wave sees as many of its blocks as waves come before it,
+    // and a part of one more
+    turn();
+    stage_ahead(whole);
+    if (wave > 0) step(kB0, s0, s1, nothing);
+    if (wave > 1) step(kB1, s1, s0, nothing);
+    if (keys > r0 + 64) turn();
+    if (wave > 2) step(kB2, s0, s1, nothing);
+    f32x16 s = wave & 1 ? s1 : s0;
+    hide(s);
+    mx = largest(s);
+    follow();
+    bf16x8 pf[2];
+    weights(s, pf);
+    add_last_values(wave, pf);
+    lds_dma::wait_vmem<0>();  // no load may land in LDS after the wave's end
     l = xor_add(l, 32);
   }
   if (query >= len) return;
@@ -377,8 +432,7 @@ using namespace prompt_detail;
 
 hipError_t launch_prompt(const PromptArgs& a, hipStream_t s) {
   // at most one partly filled tile a segment
-  const long long tiles = (long long)a.T / kRows + a.batch + 2;
-  const long long grid = tiles * a.q_heads;
+  const long long grid = ((long long)a.T / kRows + a.batch + 2) * a.q_heads;
   if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;  // the host checks
   if (a.D == 64)
     hipLaunchKernelGGL((prompt_kernel<64>), dim3((unsigned)grid), dim3(kThreads), 0, s, a);
