@@ -962,7 +962,7 @@ fgg_status prompt_attention(const void* q, const void* k, const void* v, const l
   const fgg::PromptArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
                           static_cast<const uint16_t*>(v), strides[0], strides[1], strides[2],
                           strides[3], strides[4], strides[5], starts, static_cast<uint16_t*>(out),
-                          scale, T, batch, q_heads, kv_heads, head_dim};
+                          scale, T, batch, q_heads, kv_heads, head_dim, d->num_cus};
   return launched(fn, fgg::launch_prompt(a, static_cast<hipStream_t>(stream)));
 }
 

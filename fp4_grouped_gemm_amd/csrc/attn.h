@@ -72,6 +72,7 @@ struct PromptArgs {
   uint16_t* out;          // [T, q_heads, D]
   float scale;
   int T, batch, q_heads, kv_heads, D;
+  int num_cus;  // compute units of the device
 };
 
 // Workgroups of a decode launch, from the longest length the table can hold.
