@@ -883,7 +883,7 @@ static fgg_status decode_prepare(const char* fn, const fgg_kv_cache* cache, int 
   if ((st = check_heads(fn, q_heads, cache->kv_heads, cache->head_dim)) != FGG_OK) return st;
   const long long tokens = (long long)cache->table_width * cache->page_size;
   if ((long long)cache->batch * q_heads * (tokens / 128 + 1) > (1LL << 30))
-    return fail(FGG_EUNSUPPORTED, fn, "requires batch * q_heads * table tokens / 128 <= 2^30");
+    return fail(FGG_EUNSUPPORTED, fn, "requires batch * q_heads * (table tokens / 128 + 1) <= 2^30");
   const DeviceFacts* d = current_device(fn, &st);
   if (!d) return st;
   *workgroups = fgg::decode_workgroups(cache->batch, q_heads, cache->kv_heads, tokens, d->num_cus);

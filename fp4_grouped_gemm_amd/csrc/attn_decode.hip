@@ -45,6 +45,18 @@ __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
 // An empty row has a tile too: the one that writes its zeros.
 __device__ __forceinline__ int tiles_of(int len) { return len ? (len + kTile - 1) / kTile : 1; }
 
+// The list in slices that differ by at most one tile, none of them empty (a
+// row's pieces come from consecutive slices): where one begins, and which one
+// holds a tile.  Workgroups past the last slice have nothing to do.
+__device__ __forceinline__ int slices_of(int total) { return min((int)gridDim.x, total); }
+__device__ __forceinline__ int slice_start(int i, int total) {
+  const int n = slices_of(total);
+  return i < n ? (int)((long long)i * total / n) : total;
+}
+__device__ __forceinline__ int slice_of(int tile, int total) {
+  return (int)(((long long)(tile + 1) * slices_of(total) - 1) / total);
+}
+
 // Rows of work of a KV head: its query heads by kMaxHeads.
 __device__ __forceinline__ int head_groups(const DecodeArgs& a) {
   return (a.q_heads / a.c.kv_heads + kMaxHeads - 1) / kMaxHeads;
@@ -80,7 +92,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void decode_kernel(DecodeArgs a) 
 
   // This workgroup's slice of the list, and the sequence that it begins in.
   // Each wave goes over the lengths by itself, some to a lane.
-  int b, before, total;  // `before`: tiles of one row of each earlier sequence
+  int b, before, total, pos;  // `before`: tiles of one row of each earlier sequence
   {
     const int chunk = (a.c.batch + 63) / 64;
     const int b0 = lane * chunk, b1 = min(b0 + chunk, a.c.batch);
@@ -93,7 +105,8 @@ __global__ __launch_bounds__(kThreads, kPerCu) void decode_kernel(DecodeArgs a) 
       if (lane >= off) upto += u;
     }
     total = __builtin_amdgcn_readlane(upto, 63) * rows;
-    const int first = min((int)blockIdx.x * ((total + (int)gridDim.x - 1) / (int)gridDim.x), total - 1);
+    pos = slice_start(blockIdx.x, total);
+    const int first = min(pos, total - 1);
     // the lane whose sequences hold tile `first`, then the sequence
     const int src = __builtin_ctzll(__ballot(first < upto * rows));
     before = __builtin_amdgcn_readlane(upto - sum, src);
@@ -103,9 +116,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void decode_kernel(DecodeArgs a) 
       before += n;
     }
   }
-  const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
-  int pos = (int)blockIdx.x * per;
-  const int end = min(total, pos + per);
+  const int end = slice_start(blockIdx.x + 1, total);
   const bool by_row = joins_by_row(a.c.batch * rows, (int)gridDim.x);
   if (!by_row && tid == 0) a.split[blockIdx.x].first = -1;
 
@@ -259,7 +270,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void decode_kernel(DecodeArgs a) 
     if (t0 == 0 && tid == 0) {
       if (!whole)
         a.split[by_row ? b * rows + row : (int)blockIdx.x] =
-            SplitRow{(int)blockIdx.x, (int)blockIdx.x + (n - t1 + per - 1) / per, b, head0, heads, {}};
+            SplitRow{(int)blockIdx.x, slice_of(pos + n - 1, total), b, head0, heads, {}};
       else if (by_row)
         a.split[b * rows + row].first = -1;
     }
@@ -312,24 +323,23 @@ __global__ __launch_bounds__(kThreads, kPerCu) void decode_kernel(DecodeArgs a) 
   }
 }
 
-// Joins the pieces of the rows that the slices of several workgroups share.
-// Workgroup (x, y) takes heads 2 y and 2 y + 1 of the row in place x, if there
-// is one.  The pieces of a head go to groups of
-// D / 4 lanes in turn, kAhead of them loaded at once: a row over all slices
-// (128 pieces) takes two round trips to memory.
-constexpr int kJoinThreads = 512;
+// Joins the pieces of the rows that the slices of several workgroups share:
+// kWide waves to a head of the row in place x, if there is one.  The pieces
+// of a head go to groups of D / 4 lanes in turn, kAhead of them loaded at
+// once, so that four waves take the most there can be, a row over all slices,
+// in few round trips to memory.
 constexpr int kAhead = 8;
 
-template <int D>
-__global__ __launch_bounds__(kJoinThreads) void join_kernel(DecodeArgs a) {
-  constexpr int kLanes = D / 4, kSets = kJoinThreads / 2 / kLanes;
-  __shared__ __align__(16) float red_o[2][kSets][D];
-  __shared__ float red_ml[2][kSets][2];
+template <int D, int kWide>
+__global__ __launch_bounds__(kThreads) void join_kernel(DecodeArgs a) {
+  constexpr int kLanes = D / 4, kSets = kWide * 64 / kLanes, kHeads = kWaves / kWide;
+  __shared__ __align__(16) float red_o[kHeads][kSets][D];
+  __shared__ float red_ml[kHeads][kSets][2];
   const SplitRow row = a.split[blockIdx.x];
   const int first = row.first, last = row.last;
   if (first < 0) return;
-  const int which = threadIdx.x / (kJoinThreads / 2), t = threadIdx.x % (kJoinThreads / 2);
-  const int h = min((int)blockIdx.y * 2 + which, kMaxHeads - 1);
+  const int which = threadIdx.x / (kWide * 64), t = threadIdx.x % (kWide * 64);
+  const int h = min((int)blockIdx.y * kHeads + which, kMaxHeads - 1);
   const int set = t / kLanes, d = (t % kLanes) * 4;
   float m = kNegInf, l = 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
@@ -366,7 +376,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(DecodeArgs a) {
     red_ml[which][set][1] = l;
   }
   __syncthreads();
-  if (t >= kLanes || (int)blockIdx.y * 2 + which >= row.heads) return;
+  if (t >= kLanes || (int)blockIdx.y * kHeads + which >= row.heads) return;
   float M = kNegInf;
 #pragma unroll
   for (int i = 0; i < kSets; ++i) M = fmaxf(M, red_ml[which][i][0]);
@@ -394,13 +404,17 @@ hipError_t launch(const DecodeArgs& a, int workgroups, hipStream_t s) {
   else
     hipLaunchKernelGGL((decode_kernel<D, false>), dim3(workgroups), dim3(kThreads), 0, s, a);
   hipError_t e = hipGetLastError();
-  // a row of one tile is never split: tables that hold no more need no join
+  // a row of one tile is never cut: tables that hold no more need no join
   if (e != hipSuccess || ((long long)a.c.width << a.c.page_shift) <= kTile) return e;
   const int heads = a.q_heads / a.c.kv_heads < kMaxHeads ? a.q_heads / a.c.kv_heads : kMaxHeads;
   const long long rows = (long long)a.c.batch * a.c.kv_heads *
                          ((a.q_heads / a.c.kv_heads + kMaxHeads - 1) / kMaxHeads);
-  const int places = joins_by_row((int)rows, workgroups) ? (int)rows : workgroups;
-  hipLaunchKernelGGL((join_kernel<D>), dim3(places, (heads + 1) / 2), dim3(kJoinThreads), 0, s, a);
+  // Where there are fewer rows than slices, rows have many pieces.
+  if (joins_by_row((int)rows, workgroups))
+    hipLaunchKernelGGL((join_kernel<D, kWaves>), dim3((unsigned)rows, heads), dim3(kThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((join_kernel<D, 1>), dim3(workgroups, (heads + kWaves - 1) / kWaves),
+                       dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -412,7 +426,7 @@ int decode_workgroups(int batch, int q_heads, int kv_heads, long long max_len, i
   const long long groups = (q_heads / kv_heads + kMaxHeads - 1) / kMaxHeads;
   const long long tiles = (long long)batch * kv_heads * groups * ((max_len + kTile - 1) / kTile);
   const long long cap = (long long)kPerCu * num_cus;
-  return (int)(tiles < 1 ? 1 : tiles < cap ? tiles : cap);
+  return (int)(tiles < cap ? tiles : cap);
 }
 
 size_t decode_workspace(int workgroups, int D) {
