@@ -29,13 +29,15 @@ namespace decode_detail {
 
 using namespace attn;
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
 constexpr int kWaveTokens = 32;
-constexpr int kTile = kWaves * kWaveTokens;
 constexpr int kMaxHeads = 16;  // query heads of a KV head in one row of work
 
-constexpr int kPerCu = 3;  // workgroups on a compute unit: as many as their registers allow
+// Waves of a workgroup, and workgroups on a compute unit.  Registers allow
+// three waves a SIMD: three workgroups of four waves that share the list, or
+// one of twelve that takes a whole row, of at most kWholeMax tokens.
+constexpr int kListWaves = 4, kListPerCu = 3, kTile = kListWaves * kWaveTokens;
+constexpr int kWholeWaves = 12;
+constexpr int kWholeMax = 2 * kWholeWaves * kWaveTokens;
 
 __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
   const long long cap = (long long)a.c.width << a.c.page_shift;
@@ -69,8 +71,11 @@ __device__ __host__ __forceinline__ bool joins_by_row(int rows, int workgroups) 
   return rows <= workgroups;
 }
 
-template <int D, bool FP8>
-__global__ __launch_bounds__(kThreads, kPerCu) void decode_kernel(DecodeArgs a) {
+// kWhole: one row a workgroup, nothing to join.  Else a slice of the list.
+template <int D, bool FP8, int kWaves, bool kWhole>
+__global__ __launch_bounds__(kWaves * 64, kWhole ? kWaves / 4 : kListPerCu) void decode_kernel(DecodeArgs a) {
+  constexpr int kThreads = kWaves * 64;
+  constexpr int kStep = kWaves * kWaveTokens;   // tokens that the waves take at once
   constexpr int kSteps = D / 32;                // k-steps of a QK product
   constexpr int kBlocks = D / 16;               // 16-row blocks of O^T
   constexpr int kRow = D * 2 + 32;              // LDS bytes of a staged V row (BF16)
@@ -92,8 +97,14 @@ __global__ __launch_bounds__(kThreads, kPerCu) void decode_kernel(DecodeArgs a) 
 
   // This workgroup's slice of the list, and the sequence that it begins in.
   // Each wave goes over the lengths by itself, some to a lane.
-  int b, before, total, pos;  // `before`: tiles of one row of each earlier sequence
-  {
+  int b, before, total, pos, end;  // `before`: tiles of one row of each earlier sequence
+  bool by_row = false;
+  if constexpr (kWhole) {
+    b = (int)blockIdx.x / rows;
+    before = total = 0;
+    pos = (int)blockIdx.x - b * rows;  // the row
+    end = pos + 1;
+  } else {
     const int chunk = (a.c.batch + 63) / 64;
     const int b0 = lane * chunk, b1 = min(b0 + chunk, a.c.batch);
     int sum = 0;
@@ -115,18 +126,18 @@ __global__ __launch_bounds__(kThreads, kPerCu) void decode_kernel(DecodeArgs a) 
       if (first < (before + n) * rows) break;
       before += n;
     }
+    end = slice_start(blockIdx.x + 1, total);
+    by_row = joins_by_row(a.c.batch * rows, (int)gridDim.x);
+    if (!by_row && tid == 0) a.split[blockIdx.x].first = -1;
   }
-  const int end = slice_start(blockIdx.x + 1, total);
-  const bool by_row = joins_by_row(a.c.batch * rows, (int)gridDim.x);
-  if (!by_row && tid == 0) a.split[blockIdx.x].first = -1;
 
   uint8_t* const my_stage = stage + wave * (kWaveTokens * kRow);
   while (pos < end) {
     const int len = length_of(a, b);
-    const int n = tiles_of(len);
+    const int n = kWhole ? (len + kStep - 1) / kStep : tiles_of(len);
     const int rel = pos - before * rows;
-    const int row = rel / n, t0 = rel - row * n;
-    const int t1 = min(n, t0 + end - pos);
+    const int row = kWhole ? pos : rel / n, t0 = kWhole ? 0 : rel - row * n;
+    const int t1 = kWhole ? n : min(n, t0 + end - pos);
     const int kvh = row / groups, g0 = (row - kvh * groups) * kMaxHeads;
     const int heads = min(kMaxHeads, group_heads - g0);
     const int head0 = kvh * group_heads + g0;
@@ -154,7 +165,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void decode_kernel(DecodeArgs a) 
     float m = kNegInf, l = 0.f;
 
     for (int t = t0; t < t1; ++t) {
-      const int tok0 = t * kTile + wave * kWaveTokens;
+      const int tok0 = t * kStep + wave * kWaveTokens;
       if (tok0 >= len) break;
       // lane L looks up token tok0 + L % 32: its page, or -1
       const int tok = tok0 + (lane & 31);
@@ -267,7 +278,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void decode_kernel(DecodeArgs a) 
     }
     __syncthreads();
     const bool whole = t0 == 0 && t1 == n;
-    if (t0 == 0 && tid == 0) {
+    if (!kWhole && t0 == 0 && tid == 0) {
       if (!whole)
         a.split[by_row ? b * rows + row : (int)blockIdx.x] =
             SplitRow{(int)blockIdx.x, slice_of(pos + n - 1, total), b, head0, heads, {}};
@@ -275,45 +286,33 @@ __global__ __launch_bounds__(kThreads, kPerCu) void decode_kernel(DecodeArgs a) 
         a.split[b * rows + row].first = -1;
     }
     const int piece = (int)blockIdx.x * 2 + (t0 > 0 ? 0 : 1);
-    {
-      constexpr int kPer = D * kMaxHeads / kThreads;  // outputs of a thread: 8 or 4
-      const int h = tid / (D / kPer), d = (tid % (D / kPer)) * kPer;
+    for (int x = tid; x < heads * (D / 4); x += kThreads) {
+      const int h = x / (D / 4), d = x % (D / 4) * 4;
       float M = kNegInf;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) M = fmaxf(M, ml[w][h][0]);
       const float Ms = M == kNegInf ? 0.f : M;
-      float L = 0.f, o[kPer];
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) o[i] = 0.f;
+      float L = 0.f;
+      f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
         const float f = __builtin_amdgcn_exp2f(ml[w][h][0] - Ms);
         L += f * ml[w][h][1];
-        const float* src = reinterpret_cast<const float*>(stage) + (w * kMaxHeads + h) * kOutRow + d;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) o[i] += f * src[i];
+        o += f * *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(stage) +
+                                                 (w * kMaxHeads + h) * kOutRow + d);
       }
-      if (h < heads) {
-        if (whole) {
-          const float vs = FP8 && a.c.v_scale ? a.c.v_scale[kvh] : 1.0f;
-          const float r = L == 0.f ? 0.f : vs / L;
-          uint16_t* out = a.out + ((long long)b * a.q_heads + head0 + h) * D + d;
-#pragma unroll
-          for (int i = 0; i < kPer; i += 4)
-            *reinterpret_cast<uint2*>(out + i) =
-                pack_bf16x4(o[i] * r, o[i + 1] * r, o[i + 2] * r, o[i + 3] * r);
-        } else {
-          float* out = a.part_o + ((long long)piece * kMaxHeads + h) * D + d;
-#pragma unroll
-          for (int i = 0; i < kPer; i += 4)
-            *reinterpret_cast<f32x4*>(out + i) = (f32x4){o[i], o[i + 1], o[i + 2], o[i + 3]};
-          if (d == 0) {
-            a.part_ml[(piece * kMaxHeads + h) * 2] = M;
-            a.part_ml[(piece * kMaxHeads + h) * 2 + 1] = L;
-          }
-        }
+      if (whole) {
+        const float vs = FP8 && a.c.v_scale ? a.c.v_scale[kvh] : 1.0f;
+        o *= L == 0.f ? 0.f : vs / L;
+        *reinterpret_cast<uint2*>(a.out + ((long long)b * a.q_heads + head0 + h) * D + d) =
+            pack_bf16x4(o[0], o[1], o[2], o[3]);
+      } else {
+        *reinterpret_cast<f32x4*>(a.part_o + ((long long)piece * kMaxHeads + h) * D + d) = o;
+        if (d == 0)
+          *reinterpret_cast<f32x2*>(a.part_ml + (piece * kMaxHeads + h) * 2) = (f32x2){M, L};
       }
     }
+    if constexpr (kWhole) return;
     __syncthreads();  // the stage is free again
     pos += t1 - t0;
     if (t1 == n && row == rows - 1) {
@@ -329,10 +328,11 @@ __global__ __launch_bounds__(kThreads, kPerCu) void decode_kernel(DecodeArgs a) 
 // once, so that four waves take the most there can be, a row over all slices,
 // in few round trips to memory.
 constexpr int kAhead = 8;
+constexpr int kJoinWaves = 4;
 
 template <int D, int kWide>
-__global__ __launch_bounds__(kThreads) void join_kernel(DecodeArgs a) {
-  constexpr int kLanes = D / 4, kSets = kWide * 64 / kLanes, kHeads = kWaves / kWide;
+__global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(DecodeArgs a) {
+  constexpr int kLanes = D / 4, kSets = kWide * 64 / kLanes, kHeads = kJoinWaves / kWide;
   __shared__ __align__(16) float red_o[kHeads][kSets][D];
   __shared__ float red_ml[kHeads][kSets][2];
   const SplitRow row = a.split[blockIdx.x];
@@ -397,24 +397,31 @@ __global__ __launch_bounds__(kThreads) void join_kernel(DecodeArgs a) {
       pack_bf16x4(r[0], r[1], r[2], r[3]);
 }
 
-template <int D>
+// Rows of work of a sequence.
+long long rows_of(const DecodeArgs& a) {
+  return (long long)a.c.kv_heads * ((a.q_heads / a.c.kv_heads + kMaxHeads - 1) / kMaxHeads);
+}
+
+template <int D, bool FP8>
 hipError_t launch(const DecodeArgs& a, int workgroups, hipStream_t s) {
-  if (a.c.fp8)
-    hipLaunchKernelGGL((decode_kernel<D, true>), dim3(workgroups), dim3(kThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL((decode_kernel<D, false>), dim3(workgroups), dim3(kThreads), 0, s, a);
-  hipError_t e = hipGetLastError();
-  // a row of one tile is never cut: tables that hold no more need no join
-  if (e != hipSuccess || ((long long)a.c.width << a.c.page_shift) <= kTile) return e;
+  const long long rows = a.c.batch * rows_of(a);
+  if (((long long)a.c.width << a.c.page_shift) <= kWholeMax) {
+    hipLaunchKernelGGL((decode_kernel<D, FP8, kWholeWaves, true>), dim3((unsigned)rows),
+                       dim3(kWholeWaves * 64), 0, s, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((decode_kernel<D, FP8, kListWaves, false>), dim3(workgroups),
+                     dim3(kListWaves * 64), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   const int heads = a.q_heads / a.c.kv_heads < kMaxHeads ? a.q_heads / a.c.kv_heads : kMaxHeads;
-  const long long rows = (long long)a.c.batch * a.c.kv_heads *
-                         ((a.q_heads / a.c.kv_heads + kMaxHeads - 1) / kMaxHeads);
   // Where there are fewer rows than slices, rows have many pieces.
   if (joins_by_row((int)rows, workgroups))
-    hipLaunchKernelGGL((join_kernel<D, kWaves>), dim3((unsigned)rows, heads), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((join_kernel<D, kJoinWaves>), dim3((unsigned)rows, heads),
+                       dim3(kJoinWaves * 64), 0, s, a);
   else
-    hipLaunchKernelGGL((join_kernel<D, 1>), dim3(workgroups, (heads + kWaves - 1) / kWaves),
-                       dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((join_kernel<D, 1>), dim3(workgroups, (heads + kJoinWaves - 1) / kJoinWaves),
+                       dim3(kJoinWaves * 64), 0, s, a);
   return hipGetLastError();
 }
 
@@ -425,7 +432,7 @@ using namespace decode_detail;
 int decode_workgroups(int batch, int q_heads, int kv_heads, long long max_len, int num_cus) {
   const long long groups = (q_heads / kv_heads + kMaxHeads - 1) / kMaxHeads;
   const long long tiles = (long long)batch * kv_heads * groups * ((max_len + kTile - 1) / kTile);
-  const long long cap = (long long)kPerCu * num_cus;
+  const long long cap = (long long)kListPerCu * num_cus;
   return (int)(tiles < cap ? tiles : cap);
 }
 
@@ -434,7 +441,9 @@ size_t decode_workspace(int workgroups, int D) {
 }
 
 hipError_t launch_decode(const DecodeArgs& a, int workgroups, hipStream_t s) {
-  return a.D == 64 ? launch<64>(a, workgroups, s) : launch<128>(a, workgroups, s);
+  if (a.D == 64)
+    return a.c.fp8 ? launch<64, true>(a, workgroups, s) : launch<64, false>(a, workgroups, s);
+  return a.c.fp8 ? launch<128, true>(a, workgroups, s) : launch<128, false>(a, workgroups, s);
 }
 
 }  // namespace fgg
