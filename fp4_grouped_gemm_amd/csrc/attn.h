@@ -61,6 +61,7 @@ struct DecodeArgs {
   decode_detail::SplitRow* split;  // [workgroups] rows to join
   float scale;
   int q_heads, D;
+  int num_cus;  // compute units of the device
 };
 
 struct PromptArgs {

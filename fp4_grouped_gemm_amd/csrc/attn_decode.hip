@@ -19,9 +19,11 @@
 // 4 (l / 16) + i.  Those are, packed to BF16, the B operand of
 // O^T = V^T P^T with contraction slot 8 (l / 16) + 4 a + i for token
 // 16 a + 4 (l / 16) + i: P never leaves its lane.  The A operand V^T comes
-// from LDS by transposed reads of 4 tokens each.  P is rounded to BF16 (the
-// matrix cores' input type; 2^-9 relative, as the output's own rounding);
-// scores, maxima, sums and outputs are FP32.
+// from LDS by transposed reads of 4 tokens each.  The matrix cores take BF16,
+// so a weight goes in as the sum of two BF16 values, 16 bits in all: the
+// second product costs nothing under the memory's time (221.2 against 220.3 us
+// for 128 sequences of 2000 to 8191 tokens in E4M3) and takes the weights'
+// rounding out of the result.  Scores, maxima, sums and outputs are FP32.
 #include "attn.h"
 
 namespace fgg {
@@ -34,10 +36,15 @@ constexpr int kMaxHeads = 16;  // query heads of a KV head in one row of work
 
 // Waves of a workgroup, and workgroups on a compute unit.  Registers allow
 // three waves a SIMD: three workgroups of four waves that share the list, or
-// one of twelve that takes a whole row, of at most kWholeMax tokens.
+// one of twelve that takes a whole row.  The latter needs no join and no second
+// launch; its waves take 384 tokens at once.  It is taken for tables of two
+// such steps (one row of 517 tokens: 9.1 against 8.6 us on the GPU, but 8.9
+// against 12.5 us a call with the launches), and of four where the rows fill
+// the card (256 rows of 1000 tokens 26.4 against 33.6 us, 1024 rows 100 against
+// 103 us; a single row of 1000 tokens 12.9 against 8.7 us).
 constexpr int kListWaves = 4, kListPerCu = 3, kTile = kListWaves * kWaveTokens;
 constexpr int kWholeWaves = 12;
-constexpr int kWholeMax = 2 * kWholeWaves * kWaveTokens;
+constexpr int kWholeStep = kWholeWaves * kWaveTokens;
 
 __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
   const long long cap = (long long)a.c.width << a.c.page_shift;
@@ -239,9 +246,17 @@ __global__ __launch_bounds__(kWaves * 64, kWhole ? kWaves / 4 : kListPerCu) void
         sum += p[i];
       }
       l = l * alpha + sum;  // of this lane's tokens; the quads are added at the end
-      const bf16x8 pf = __builtin_bit_cast(
-          bf16x8, (u32x4){pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]),
-                          pack_bf16(p[6], p[7])});
+      // Each weight as the sum of two BF16 values: its upper half, and what is
+      // left plus 2^-23 of it, which keeps the second one above zero (0 times
+      // an infinite value would be NaN).
+      u32x4 ph, pl;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x = __float_as_uint(p[2 * i]), y = __float_as_uint(p[2 * i + 1]);
+        ph[i] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+        pl[i] = pack_bf16(fmaf(p[2 * i], 1.f + 0x1p-23f, -__uint_as_float(x & 0xFFFF0000u)),
+                          fmaf(p[2 * i + 1], 1.f + 0x1p-23f, -__uint_as_float(y & 0xFFFF0000u)));
+      }
       // values through LDS (rows of BF16)
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
@@ -261,7 +276,8 @@ __global__ __launch_bounds__(kWaves * 64, kWhole ? kWaves / 4 : kListPerCu) void
         const u32x2 lo = lds_read_tr(src), hi = lds_read_tr(src + 16 * kRow);
         const bf16x8 vf = __builtin_bit_cast(bf16x8, (u32x4){lo[0], lo[1], hi[0], hi[1]});
         acc[i] *= alpha;
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf, acc[i], 0, 0, 0);
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, __builtin_bit_cast(bf16x8, ph), acc[i], 0, 0, 0);
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, __builtin_bit_cast(bf16x8, pl), acc[i], 0, 0, 0);
       }
       __builtin_amdgcn_wave_barrier();
     }
@@ -405,7 +421,8 @@ long long rows_of(const DecodeArgs& a) {
 template <int D, bool FP8>
 hipError_t launch(const DecodeArgs& a, int workgroups, hipStream_t s) {
   const long long rows = a.c.batch * rows_of(a);
-  if (((long long)a.c.width << a.c.page_shift) <= kWholeMax) {
+  const long long tokens = (long long)a.c.width << a.c.page_shift;
+  if (tokens <= (rows >= a.num_cus ? 4 : 2) * kWholeStep) {
     hipLaunchKernelGGL((decode_kernel<D, FP8, kWholeWaves, true>), dim3((unsigned)rows),
                        dim3(kWholeWaves * 64), 0, s, a);
     return hipGetLastError();

@@ -516,8 +516,8 @@ fgg_status rope_kv_append(const fgg_kv_cache* cache, const void* q, const void* 
  *            contents need no initialisation and are free after the call's
  *            work on `stream` is done.
  *
- * Scores, maxima, sums and outputs are FP32; the weights p_t are rounded to
- * BF16 for the product with V.  What the cache holds past a sequence's
+ * Scores, maxima, sums and outputs are FP32; the weights p_t enter the
+ * product with V to 16 bits, as sums of two BF16 values.  What the cache holds past a sequence's
  * length never reaches an output, NaN included.
  */
 fgg_status paged_decode_attention_workspace(const fgg_kv_cache* cache, int q_heads, size_t* bytes);
@@ -537,7 +537,8 @@ fgg_status paged_decode_attention(const fgg_kv_cache* cache, const void* q, long
  *            device only.  Tokens of no prompt get zeros.
  *   out      BF16 [T, q_heads, head_dim]
  *
- * Arithmetic as paged_decode_attention; keys and values that a query does
+ * Scores, maxima, sums and outputs are FP32; the weights are rounded to BF16
+ * for the product with V.  Keys and values that a query does
  * not attend to never reach its output, infinities and NaN included.
  */
 fgg_status prompt_attention(const void* q, const void* k, const void* v, const long long* strides,
