@@ -26,7 +26,7 @@ _KV_CACHE = struct.Struct("@PPPPPqqqqqqqiiiiiii")
 _STRIDES = struct.Struct("@6q")
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 _BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 _LIB = None
 _WORKSPACE = {}  # bytes by device and sizes
 
@@ -50,64 +50,76 @@ def _lib():
     return _LIB
 
 
-def _gpu(t, name, dtype, dim, device=None):
-    """Checks a GPU tensor; returns the index of its device."""
+def _bad(t, name, dtype, dim, device):
+    """Raises what is wrong with a tensor that is not `dim`-D of `dtype` on
+    `device` (None: any GPU)."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != dim:
         raise ValueError(f"{name} must be a {dim}-D {dtype} tensor")
-    d = t.get_device()
-    if d < 0 or not t.is_cuda:
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if device is not None and d != device:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
-    return d
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
 
 
+# (The checks read each attribute once: they are most of a small call's time.)
 def _heads(t, name, device=None):
-    """A BF16 [rows, heads, head_dim] operand, head_dim contiguous: its device
-    and its strides."""
-    d = _gpu(t, name, _BF16, 3, device)
-    st = t.stride()
+    """Checks a BF16 [rows, heads, head_dim] operand, head_dim contiguous: its
+    device and its strides."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16:
+        _bad(t, name, _BF16, 3, device)
+    d, st = t.get_device(), t.stride()
+    if len(st) != 3 or d < 0 or (device is not None and d != device):
+        _bad(t, name, _BF16, 3, device)
     if st[2] != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
     return d, st
 
 
+def _matrix(t, name, dtype, device):
+    """Checks a 2-D tensor, its last dimension contiguous: shape and row stride."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device:
+        _bad(t, name, dtype, 2, device)
+    shape, st = t.shape, t.stride()
+    if len(shape) != 2:
+        _bad(t, name, dtype, 2, device)
+    if st[1] != 1 and shape[1] != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return shape, st[0]
+
+
 def _vector(t, name, n, device, dtype=_I32):
-    _gpu(t, name, dtype, 1, device)
-    if t.shape[0] != n or not t.is_contiguous():
+    """Checks a contiguous vector of n values (None: of any length): its address."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device or t.dim() != 1:
+        _bad(t, name, dtype, 1, device)
+    if (n is not None and t.shape[0] != n) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape ({n},)")
     return t.data_ptr()
 
 
 def _cache(k_cache, v_cache, page_table, k_scale, v_scale, device):
-    """Checks a cache: the packed fgg_kv_cache and its (pages, kv_heads,
-    page_size, head_dim), batch and table width."""
+    """Checks a cache: the packed fgg_kv_cache and its kv_heads, page_size,
+    head_dim, batch and table width."""
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         if not isinstance(t, torch.Tensor) or t.dim() != 4:
             raise ValueError(f"{name} must be a tensor [pages, kv_heads, page_size, head_dim]")
-        if t.get_device() != device or not t.is_cuda:
+        if t.get_device() != device:
             raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
     shape, dtype = k_cache.shape, k_cache.dtype
-    if dtype != v_cache.dtype or shape != v_cache.shape:
+    if dtype is not v_cache.dtype or shape != v_cache.shape:
         raise ValueError("k_cache and v_cache must have one dtype and shape")
     fp8 = dtype in _CODES
-    if not fp8 and dtype != _BF16:
+    if not fp8 and dtype is not _BF16:
         raise ValueError(f"a cache holds bfloat16 or E4M3 codes (float8_e4m3fn / uint8), got {dtype}")
     ks, vs = k_cache.stride(), v_cache.stride()
     if ks[3] != 1 or vs[3] != 1:
         raise ValueError("k_cache and v_cache must be contiguous in their last dimension")
     pages, heads, page_size, dim = shape
-    _gpu(page_table, "page_table", _I32, 2, device)
-    batch, width = page_table.shape
-    ts = page_table.stride()
-    if ts[1] != 1 and width != 1:
-        raise ValueError("page_table must be contiguous in its last dimension")
+    (batch, width), row = _matrix(page_table, "page_table", _I32, device)
     if not fp8 and (k_scale is not None or v_scale is not None):
         raise ValueError("k_scale and v_scale go with an E4M3 cache")
     k_sc = 0 if k_scale is None else _vector(k_scale, "k_scale", heads, device, _F32)
     v_sc = 0 if v_scale is None else _vector(v_scale, "v_scale", heads, device, _F32)
     packed = _KV_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_sc, v_sc,
-                            page_table.data_ptr(), ts[0], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
+                            page_table.data_ptr(), row, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
                             KV_E4M3 if fp8 else KV_BF16, pages, heads, page_size, dim, batch, width)
     return packed, heads, page_size, dim, batch, width
 
@@ -117,7 +129,7 @@ def _elsewhere(device, stream):
     that makes them so, so that memory allocated for the call belongs to the
     stream that uses it."""
     if stream is None:
-        return None if torch.cuda.current_device() == device else torch.cuda.device(device)
+        return None if _current_device() == device else torch.cuda.device(device)
     if stream.device.index != device:
         raise ValueError(f"stream is on {stream.device}, expected cuda:{device}")
     return torch.cuda.stream(stream)
@@ -162,10 +174,9 @@ def rope_kv_append(q, k, v, cos_sin, positions, page_table, k_cache, v_cache, *,
     T, hq, d = q.shape
     if d != dim or k.shape != (T, hk, d) or v.shape != (T, hk, d):
         raise ValueError(f"q must be [T, Hq, {dim}], k and v [T, {hk}, {dim}] as the cache")
-    _gpu(cos_sin, "cos_sin", _F32, 2, dev)
-    if not cos_sin.is_contiguous():
+    (turns, rot), row = _matrix(cos_sin, "cos_sin", _F32, dev)
+    if row != rot and turns != 1:
         raise ValueError("cos_sin must be contiguous")
-    turns, rot = cos_sin.shape
     pos = _vector(positions, "positions", T, dev)
     ids = None if seq_ids is None else _vector(seq_ids, "seq_ids", T, dev)
     res = _result(out, q, (T, hq, d), dev)
@@ -208,7 +219,8 @@ def paged_decode_attention(q, k_cache, v_cache, page_table, lengths, *, scale=No
             if len(_WORKSPACE) >= 4096:
                 _WORKSPACE.clear()
             n = _WORKSPACE[sizes] = need.value
-        work = torch.empty(n, dtype=torch.uint8, device=q.device)
+        # (a call that needs no workspace is given its output's address)
+        work = torch.empty(n, dtype=torch.uint8, device=q.device) if n else res
         _check(lib.paged_decode_attention(cache, q.data_ptr(), qs[0], qs[1], lens,
                                           d ** -0.5 if scale is None else float(scale),
                                           res.data_ptr(), hq, work.data_ptr(), n, _raw_stream(dev)))
@@ -233,14 +245,14 @@ def prompt_attention(q, k, v, starts, *, scale=None, out=None, stream=None):
     hk = k.shape[1]
     if k.shape != (T, hk, d) or v.shape != (T, hk, d):
         raise ValueError(f"k and v must be [{T}, Hkv, {d}] as q")
-    _gpu(starts, "starts", _I32, 1, dev)
+    starts_ptr = _vector(starts, "starts", None, dev)
     batch = starts.shape[0] - 1
-    if batch < 1 or not starts.is_contiguous():
-        raise ValueError("starts must be a contiguous int32 tensor of shape (B + 1,), B >= 1")
+    if batch < 1:
+        raise ValueError("starts must be an int32 tensor of shape (B + 1,), B >= 1")
     res = _result(out, q, (T, hq, d), dev)
     if T:
         strides = _STRIDES.pack(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1])
         _check(_lib().prompt_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), strides,
-                                       starts.data_ptr(), d ** -0.5 if scale is None else float(scale),
+                                       starts_ptr, d ** -0.5 if scale is None else float(scale),
                                        res.data_ptr(), T, batch, hq, hk, d, _raw_stream(dev)))
     return res

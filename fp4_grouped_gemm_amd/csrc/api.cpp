@@ -886,7 +886,6 @@ static fgg_status decode_prepare(const char* fn, const fgg_kv_cache* cache, int 
     return fail(FGG_EUNSUPPORTED, fn, "requires batch * q_heads * (table tokens / 128 + 1) <= 2^30");
   const DeviceFacts* d = current_device(fn, &st);
   if (!d) return st;
-  a->num_cus = d->num_cus;
   *workgroups = fgg::decode_workgroups(cache->batch, q_heads, cache->kv_heads, tokens, d->num_cus);
   return FGG_OK;
 }

@@ -61,7 +61,6 @@ struct DecodeArgs {
   decode_detail::SplitRow* split;  // [workgroups] rows to join
   float scale;
   int q_heads, D;
-  int num_cus;  // compute units of the device
 };
 
 struct PromptArgs {
@@ -76,7 +75,8 @@ struct PromptArgs {
   int num_cus;  // compute units of the device
 };
 
-// Workgroups of a decode launch, from the longest length the table can hold.
+// Workgroups that share the list of a decode launch, from the longest length
+// the table can hold; 0: each row has one of its own.
 int decode_workgroups(int batch, int q_heads, int kv_heads, long long max_len, int num_cus);
 // Bytes of its workspace (part_o, part_ml, split) for that many workgroups.
 size_t decode_workspace(int workgroups, int D);

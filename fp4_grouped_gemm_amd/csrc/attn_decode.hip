@@ -413,16 +413,15 @@ __global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(DecodeArgs a) {
       pack_bf16x4(r[0], r[1], r[2], r[3]);
 }
 
-// Rows of work of a sequence.
-long long rows_of(const DecodeArgs& a) {
-  return (long long)a.c.kv_heads * ((a.q_heads / a.c.kv_heads + kMaxHeads - 1) / kMaxHeads);
+// Rows of work of a batch.
+long long rows_of(int batch, int q_heads, int kv_heads) {
+  return (long long)batch * kv_heads * ((q_heads / kv_heads + kMaxHeads - 1) / kMaxHeads);
 }
 
 template <int D, bool FP8>
 hipError_t launch(const DecodeArgs& a, int workgroups, hipStream_t s) {
-  const long long rows = a.c.batch * rows_of(a);
-  const long long tokens = (long long)a.c.width << a.c.page_shift;
-  if (tokens <= (rows >= a.num_cus ? 4 : 2) * kWholeStep) {
+  const long long rows = rows_of(a.c.batch, a.q_heads, a.c.kv_heads);
+  if (workgroups == 0) {
     hipLaunchKernelGGL((decode_kernel<D, FP8, kWholeWaves, true>), dim3((unsigned)rows),
                        dim3(kWholeWaves * 64), 0, s, a);
     return hipGetLastError();
@@ -447,8 +446,9 @@ hipError_t launch(const DecodeArgs& a, int workgroups, hipStream_t s) {
 using namespace decode_detail;
 
 int decode_workgroups(int batch, int q_heads, int kv_heads, long long max_len, int num_cus) {
-  const long long groups = (q_heads / kv_heads + kMaxHeads - 1) / kMaxHeads;
-  const long long tiles = (long long)batch * kv_heads * groups * ((max_len + kTile - 1) / kTile);
+  const long long rows = rows_of(batch, q_heads, kv_heads);
+  if (max_len <= (rows >= num_cus ? 4 : 2) * kWholeStep) return 0;
+  const long long tiles = rows * ((max_len + kTile - 1) / kTile);
   const long long cap = (long long)kListPerCu * num_cus;
   return (int)(tiles < cap ? tiles : cap);
 }

@@ -512,7 +512,8 @@ fgg_status rope_kv_append(const fgg_kv_cache* cache, const void* q, const void* 
  *   out      BF16 [batch, q_heads, head_dim]
  *   workspace  device memory of at least the bytes that
  *            paged_decode_attention_workspace gives for this cache (its
- *            sizes only: no pointer is read) and q_heads, 16-byte aligned; its
+ *            sizes only: no pointer is read) and q_heads, 16-byte aligned and
+ *            not null even where that is 0 (short tables need none); its
  *            contents need no initialisation and are free after the call's
  *            work on `stream` is done.
  *
