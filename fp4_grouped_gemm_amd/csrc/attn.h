@@ -105,8 +105,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // three bits of mantissa).
 template <bool HIGH>
 __device__ __forceinline__ uint32_t fp8x2_to_bf16(uint32_t w) {
-  const f32x2 f = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, HIGH);
-  return pack_bf16(f[0], f[1]);
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HIGH));
 }
 // 8 codes -> 8 BF16 values.
 __device__ __forceinline__ u32x4 fp8x8_to_bf16(u32x2 w) {

@@ -78,6 +78,14 @@ __device__ __host__ __forceinline__ bool joins_by_row(int rows, int workgroups) 
   return rows <= workgroups;
 }
 
+// A load of what this launch does not read again.  Keys and values of a batch
+// are far more than the caches hold, and a load that does not displace what
+// they hold reads faster: 64 sequences of 12000 to 32768 tokens 804 against 891
+// us (6.8 against 6.1 TB/s), 96 of 1 to 6000 65 against 73 us.
+__device__ __forceinline__ u32x4 once(const uint8_t* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+}
+
 // kWhole: one row a workgroup, nothing to join.  Else a slice of the list.
 template <int D, bool FP8, int kWaves, bool kWhole>
 __global__ __launch_bounds__(kWaves * 64, kWhole ? kWaves / 4 : kListPerCu) void decode_kernel(DecodeArgs a) {
@@ -193,14 +201,13 @@ __global__ __launch_bounds__(kWaves * 64, kWhole ? kWaves / 4 : kListPerCu) void
         const int pg = __shfl(safe, src, 64), sl = __shfl(slot, src, 64);
         const uint8_t* p = kbase + pg * a.c.k_page + sl * a.c.k_token + quad * 16;
 #pragma unroll
-        for (int s = 0; s < kVB / 64; ++s) kw[g][s] = *reinterpret_cast<const u32x4*>(p + s * 64);
+        for (int s = 0; s < kVB / 64; ++s) kw[g][s] = once(p + s * 64);
       }
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int src = i * (64 / kLanesPerRow) + lane / kLanesPerRow;
         const int pg = __shfl(safe, src, 64), sl = __shfl(slot, src, 64);
-        vw[i] = *reinterpret_cast<const u32x4*>(vbase + pg * a.c.v_page + sl * a.c.v_token +
-                                                (lane % kLanesPerRow) * 16);
+        vw[i] = once(vbase + pg * a.c.v_page + sl * a.c.v_token + (lane % kLanesPerRow) * 16);
       }
       // scores
       float s[8];
