@@ -955,8 +955,8 @@ fgg_status prompt_attention(const void* q, const void* k, const void* v, const l
     return fail(FGG_EINVAL, fn, "requires 1 <= batch <= 2^20, got %d", batch);
   if (!aligned(out, 16)) return fail(FGG_EALIGN, fn, "out must be 16-byte aligned");
   if (!aligned(starts, 4)) return fail(FGG_EALIGN, fn, "starts must be 4-byte aligned");
-  if (((long long)T / 64 + batch + 2) * q_heads > 0x7FFFFFFFLL)
-    return fail(FGG_EUNSUPPORTED, fn, "requires (T / 64 + batch + 2) * q_heads < 2^31");
+  if (((long long)T / 32 + batch + 2) * q_heads > 0x7FFFFFFFLL)
+    return fail(FGG_EUNSUPPORTED, fn, "requires (T / 32 + batch + 2) * q_heads < 2^31");
   const DeviceFacts* d = current_device(fn, &st);
   if (!d) return st;
   const fgg::PromptArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),

@@ -33,8 +33,9 @@ using namespace attn;
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-// Queries of a workgroup whose waves are split KG ways over the keys.
-constexpr int rows_of(int KG) { return 32 * kWaves / KG; }
+// Queries of a workgroup whose waves take HP heads and are split KG ways over
+// the keys.
+constexpr int rows_of(int KG, int HP) { return 32 * kWaves / (KG * HP); }
 constexpr float kSlack = 8.f;       // weights may reach 2^kSlack before a rescaling
 
 // Segment i of the packed tokens: 0 is what lies before the first prompt,
@@ -111,10 +112,11 @@ __device__ __forceinline__ float half_max(float v) {
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-template <int D, int KG>
+template <int D, int KG, int HP>
 __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
-  constexpr int kGroups = kWaves / KG;  // of 32 queries
-  constexpr int kRows = rows_of(KG);
+  static_assert(HP == 1 || KG == 1, "waves take several heads or several parts of the keys");
+  constexpr int kRows = rows_of(KG, HP);
+  constexpr int kGroups = kRows / 32;  // of 32 queries
   constexpr int kSteps = D / 16;    // k-steps of a QK product
   constexpr int kBlocks = D / 32;   // 32-row blocks of O^T
   constexpr int kRowBytes = D * 2;
@@ -127,13 +129,14 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
-  const int group = wave % kGroups, part = wave / kGroups;  // queries, keys
+  const int group = wave % kGroups, part = KG == 1 ? 0 : wave / kGroups;  // queries, keys
 
   // the row tile of this workgroup: heads fastest, so that the workgroups of
   // one KV head meet on the same XCDs' L2
-  const int hid = (int)blockIdx.x % a.q_heads, item = (int)blockIdx.x / a.q_heads;
+  const int head_sets = a.q_heads / HP;
+  const int hid = (int)blockIdx.x % head_sets, item = (int)blockIdx.x / head_sets;
   const int kvh = hid % a.kv_heads;
-  const int head = kvh * (a.q_heads / a.kv_heads) + hid / a.kv_heads;
+  const int head = kvh * (a.q_heads / a.kv_heads) + hid / a.kv_heads * HP + wave / kGroups % HP;
   // Each wave looks for it by itself.  Tiles with many keys come first.
   int seg, lo, hi, len, tile;
   const int segs = a.batch + 2;
@@ -458,7 +461,7 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
       main_turn(std::integral_constant<int, 0>{});
       main_turn(std::integral_constant<int, 2>{});
     }
-    for (; u < whole; u += 2) {
+    for (; u + 2 <= whole; u += 2) {
       turn();
       stage_ahead(u);
       if constexpr (KG == 1) {
@@ -469,23 +472,32 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
         s0 = s1;
       }
     }
-    // the diagonal: a group of queries sees as many of its blocks as groups come
-    // before it, and a part of one more
+    // The diagonal: a group of queries sees as many of its blocks as groups come
+    // before it, and a part of one more, its last.
     turn();
-    const int ring = whole & 3;
+    int ring = u & 3;
     bf16x8 pf[2];
     if constexpr (KG == 1) {
-      stage_ahead(whole);
-      if (group > 0) step(ring, ring + 1, s0, s1, nothing);
-      if (group > 1) step(ring + 1, ring + 2, s1, s0, nothing);
-      if (keys > r0 + 64) turn();
-      if (group > 2) step(ring + 2, ring + 3, s0, s1, nothing);
-      f32x16 s = group & 1 ? s1 : s0;
-      hide(s);
-      mx = largest(s);
+      if constexpr (kGroups == 1) {
+        if (u < whole) {
+          step(ring, ring + 1, s0, s1, nothing);
+          s0 = s1;
+          ++ring;
+        }
+      } else {
+        if (kGroups > 2) stage_ahead(whole);
+        if (group > 0) step(ring, ring + 1, s0, s1, nothing);
+        if (group > 1) step(ring + 1, ring + 2, s1, s0, nothing);
+        if (kGroups > 2 && keys > r0 + 64) turn();
+        if (group > 2) step(ring + 2, ring + 3, s0, s1, nothing);
+        if (group & 1) s0 = s1;
+        ring += group;
+      }
+      hide(s0);
+      mx = largest(s0);
       follow();
-      weights(s, pf);
-      add_last_values(ring + group, pf);
+      weights(s0, pf);
+      add_last_values(ring, pf);
     } else {
       if (part == group) {
         hide(s0);
@@ -504,7 +516,7 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
     if constexpr (KG == 2) {
       // the second part of the keys joins the first
       lds_dma::lds_barrier();
-      float* to = reinterpret_cast<float*>(lds) + group * ((kBlocks * 16 + 2) * 64) + lane;
+      float* to = reinterpret_cast<float*>(lds) + wave % 2 * ((kBlocks * 16 + 2) * 64) + lane;
       if (part) {
         to[0] = m;
         to[64] = l;
@@ -545,25 +557,35 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
 
 using namespace prompt_detail;
 
-template <int D, int KG>
+template <int D, int KG, int HP>
 hipError_t launch(const PromptArgs& a, hipStream_t s) {
   // at most one partly filled tile a segment
-  const long long grid = ((long long)a.T / rows_of(KG) + a.batch + 2) * a.q_heads;
+  const long long grid = ((long long)a.T / rows_of(KG, HP) + a.batch + 2) * (a.q_heads / HP);
   if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;  // the host checks
-  hipLaunchKernelGGL((prompt_kernel<D, KG>), dim3((unsigned)grid), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((prompt_kernel<D, KG, HP>), dim3((unsigned)grid), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
-hipError_t launch_prompt(const PromptArgs& a, hipStream_t s) {
-  // The tiles of 128 queries, at 128 x 128 keys and values loaded once for
-  // four waves, are the cheaper ones a query; where they would leave compute
-  // units without work or with one (long) tile each, halves of them, split over
-  // the keys, spread better.  Measured (D = 128): 8 heads of 4001 tokens 60
-  // against 49 us, 32 heads of 1000 22 against 20 us, but 32 heads of 2048 46
-  // against 52 us and 12288 tokens 635 against 736 us.
+template <int D>
+hipError_t launch(const PromptArgs& a, hipStream_t s) {
+  // A workgroup with 128 (head, query) rows loads a key for four waves.  Where
+  // that would leave compute units without work or with one (long) item each,
+  // halves of them, split over the keys, spread better.  Measured (D = 128): 8
+  // heads of 4001 tokens 60 against 49 us, 32 heads of 1000 22 against 20 us,
+  // but 32 heads of 2048 46 against 52 us and 12288 tokens 635 against 736 us.
   const bool split = (long long)((a.T + 127) / 128) * a.q_heads <= a.num_cus;
-  if (a.D == 64) return split ? launch<64, 2>(a, s) : launch<64, 1>(a, s);
-  return split ? launch<128, 2>(a, s) : launch<128, 1>(a, s);
+  if (split) return launch<D, 2, 1>(a, s);
+  // Its waves take heads of one KV head, as many of four as divide the group:
+  // fewer queries then make up the rows, and less is computed for nothing on
+  // the diagonal (24 prompts of 17 to 1501 tokens, D = 64: 54 against 59 us;
+  // nothing gained on 8192 tokens, nor where the keys are split).
+  const int group = a.q_heads / a.kv_heads;
+  if (group % 4 == 0) return launch<D, 1, 4>(a, s);
+  return group % 2 == 0 ? launch<D, 1, 2>(a, s) : launch<D, 1, 1>(a, s);
+}
+
+hipError_t launch_prompt(const PromptArgs& a, hipStream_t s) {
+  return a.D == 64 ? launch<64>(a, s) : launch<128>(a, s);
 }
 
 }  // namespace fgg
