@@ -145,6 +145,34 @@ def test_decode_split_rows_are_joined(lens):
     _decode(lens, 4, 1, 64, 16, True, seed=len(lens))
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_edges_beside_a_long_row(d, fp8):
+    """A long sequence in the batch: the lengths' edges where workgroups share
+    the rows instead of taking one each."""
+    _decode(EDGES + [2600], 6, 2, d, 16, fp8, seed=d)
+
+
+@pytest.mark.parametrize("tokens", [384, 385, 767, 768, 769, 1536, 1537])
+def test_decode_table_widths(tokens):
+    """Around the widths up to which a workgroup takes a whole row, for few rows
+    and for as many as there are compute units."""
+    _decode([tokens, 1, 300], 4, 2, 64, 1, seed=tokens)
+    lens = [tokens] + [int(x) for x in np.random.default_rng(tokens).integers(0, 90, 139)]
+    a, out = _decode(lens, 2, 2, 64, 1, seed=tokens, check=False)
+    _check_decode(a, out, rows=[0, 1, 2, 70, 138, 139])
+
+
+def test_decode_more_rows_than_slices():
+    """Rows of many more sequences than there are workgroups, some of them shared."""
+    lens = [int(x) for x in np.random.default_rng(5).integers(0, 300, 420)]
+    lens[3], lens[200], lens[419] = 3000, 2000, 2500
+    a, out = _decode(lens, 4, 2, 64, 32, seed=6, check=False)
+    _check_decode(a, out, rows=[0, 1, 2, 3, 4, 199, 200, 201, 300, 418, 419])
+    a, out = _decode(lens, 2, 2, 128, 16, True, seed=7, check=False)
+    _check_decode(a, out, rows=[0, 3, 200, 419])
+
+
 def test_decode_many_sequences():
     """More sequences than a workgroup has threads: several lengths a thread."""
     rng = np.random.default_rng(3)
@@ -420,6 +448,36 @@ def test_prompt_head_groups(hq, hk):
     for d in (64, 128):
         a, out = _prompt([100, 45], hq, hk, d, seed=hq)
         _check_prompt(a, out)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hk", [(16, 4), (24, 4), (14, 2), (16, 16)])
+def test_prompt_batches_that_fill_the_card(hq, hk, d):
+    """Enough rows for whole tiles, whose waves take four, two or one heads of a
+    KV head: every length of the last tile, short and long prompts."""
+    lens = [1, 2, 31, 32, 33, 63, 64, 65, 95, 96, 97, 127, 128, 129, 160, 0, 191, 192, 193, 224, 255, 257, 288, 321,
+            480, 1, 640, 17]
+    a, out = _prompt(lens, hq, hk, d, seed=hq + d)
+    keep = sorted({0, 1, hq // 2, hq - 1})
+    want, mag = oa.prompt_attention(_f64(a["q"])[:, keep], _f64(a["k"])[:, [h // (hq // hk) for h in keep]],
+                                    _f64(a["v"])[:, [h // (hq // hk) for h in keep]], a["starts"].cpu().numpy(), d ** -0.5)
+    _close(out[:, keep], want, mag, f"hq={hq} hk={hk}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hk", [(16, 4), (16, 8), (16, 16)])
+def test_prompt_later_tokens_never_arrive_in_whole_tiles(hq, hk, d):
+    torch = _torch()
+    a, base = _prompt([900, 1000, 300], hq, hk, d, seed=8)
+    per = hq // hk
+    for at in (900, 900 + 33, 900 + 130, 900 + 999):
+        v = a["v"].clone()
+        v[at, 1, 5], v[at, 1, 6] = float("inf"), float("nan")
+        out = fgg.prompt_attention(**dict(a, v=v))
+        want = base.clone()
+        want[at:1900, per:2 * per, 5], want[at:1900, per:2 * per, 6] = float("inf"), float("nan")
+        same = (out == want) | (torch.isnan(out) & torch.isnan(want))
+        assert same.all(), f"value at {at}: {(~same).sum()} differ"
 
 
 def test_prompt_many_short_ones():
