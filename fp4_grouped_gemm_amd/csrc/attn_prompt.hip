@@ -31,6 +31,7 @@
 // count as zeros in the product and are added by hand to the queries that
 // see them.
 #include "attn.h"
+#include "attn_layout.h"
 
 #include <type_traits>
 
@@ -39,7 +40,7 @@ namespace prompt_detail {
 
 using namespace attn;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = attn_layout::kThreads;
 constexpr int kWaves = kThreads / 64;
 // Queries of a workgroup whose waves take HP heads and are split KG ways over
 // the keys.
@@ -64,20 +65,6 @@ __device__ __forceinline__ uint32_t odd_bits(uint32_t w) { return (w & 0x7F807F8
 __device__ __forceinline__ uint32_t without_odd(uint32_t w) {
   const uint32_t odd = odd_bits(w);
   return w & ~((odd & 0x8000u ? 0xFFFFu : 0u) | (odd & 0x80000000u ? 0xFFFF0000u : 0u));
-}
-
-// LDS layout of a staged tile: row r at r D 2 bytes, its 16-byte chunk c at
-// chunk c ^ key(r), so that what one cycle of a fragment read touches lies in
-// different banks.  K: 16 lanes read one chunk index of 16 rows that differ in
-// their low four bits.  V (transposed reads): groups of lanes read 64 bytes
-// of four consecutive rows, or 32 bytes of eight.
-template <int D>
-__device__ __forceinline__ int k_key(int r) {
-  return D == 128 ? r & 15 : (r >> 1) & 7;
-}
-template <int D>
-__device__ __forceinline__ int v_key(int r) {
-  return D == 128 ? ((r & 3) << 2) | ((r >> 1) & 2) : ((r << 1) & 4) | ((r >> 1) & 2);
 }
 
 // A direct load into LDS as lds_dma::dma16, except that the compiler may move
@@ -239,14 +226,12 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
     const uint16_t* vp = a.v + (long long)lo * a.v_token + kvh * a.v_head;
     const int keys = min(len, r0 + kRows);  // that any query of the workgroup sees
 
-    // Staging: a load of the four waves fills 256 chunks in LDS order; a lane
-    // fetches the chunk that belongs at its place.  A load moves a multiple of
-    // 16 rows, which leaves the chunk keys as they are.  Rows past the last key
-    // are not loaded and read as zeros.
-    const int row_in = tid / kChunks, chunk_in = tid % kChunks;
+    // Staging: a load of the four waves fills 256 chunks of a block (see the
+    // layout's header).  Rows past the last key are not loaded and read as zeros.
+    const int row_in = tid / kChunks;
     constexpr int kRowsPerLoad = kThreads / kChunks;
-    const uint32_t k_at = (uint32_t)(row_in * a.k_token * 2) + ((chunk_in ^ k_key<D>(row_in)) << 4);
-    const uint32_t v_at = (uint32_t)(row_in * a.v_token * 2) + ((chunk_in ^ v_key<D>(row_in)) << 4);
+    const uint32_t k_at = attn_layout::stage_off(D, tid, false, a.k_token);
+    const uint32_t v_at = attn_layout::stage_off(D, tid, true, a.v_token);
     const uint32_t k_load = (uint32_t)(kRowsPerLoad * 2) * (uint32_t)a.k_token;
     const uint32_t v_load = (uint32_t)(kRowsPerLoad * 2) * (uint32_t)a.v_token;
     const uint32_t lds0 = lds_dma::lds_addr(lds) + wave * 1024;
@@ -254,7 +239,7 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
                      int block) __attribute__((always_inline)) {
       const int left = min(keys - block * 32, 32);
       const i32x4 rs = lds_dma::rsrc(p + (long long)block * 32 * stride,
-                                     left > 0 ? (uint32_t)((left - 1) * (uint32_t)stride + D) * 2 : 0u);
+                                     attn_layout::stage_bytes(D, left, stride));
 #pragma unroll
       for (int i = 0; i < kLoads; ++i)
         dma16(rs, lds0 + (ring + (block & 3)) * kBlockBytes + i * (kThreads * 16),
@@ -267,11 +252,9 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
     uint32_t k_lds[kSteps];
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
-      k_lds[k] = lds_dma::lds_addr(lds) + part * kBlockBytes + col * kRowBytes +
-                 (((2 * k + half) ^ k_key<D>(col)) << 4);
+      k_lds[k] = lds_dma::lds_addr(lds) + part * kBlockBytes + attn_layout::k_read(D, lane, k);
       asm("" : "+v"(k_lds[k]));  // kept whole: a block's place is the read's constant offset
     }
-    const int v_row = half * 4 + ((lane & 15) >> 2);
 
     const int whole = r0 / 32;  // blocks that all queries of the workgroup see whole
     // The steps of a block of 32 keys: its scores, the largest one, the
@@ -349,13 +332,8 @@ __global__ __launch_bounds__(kThreads, 2) void prompt_kernel(PromptArgs a) {
     // V^T operand of 16 keys (half of a block) and 32 of its dims
     auto value = [&](auto block, int k, int i) __attribute__((always_inline)) {
       const uint8_t* vs = lds + (4 + part + block) * kBlockBytes;
-      u32x2 x[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = k * 16 + e * 8 + v_row;
-        const int c = i * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-        x[e] = lds_read_tr(vs + r * kRowBytes + ((c ^ v_key<D>(r)) << 4) + (lane & 1) * 8);
-      }
+      const u32x2 x[2] = {lds_read_tr(vs + attn_layout::v_read(D, lane, k, i, 0)),
+                          lds_read_tr(vs + attn_layout::v_read(D, lane, k, i, 1))};
       return (u32x4){x[0][0], x[0][1], x[1][0], x[1][1]};
     };
     auto add_values = [&](auto block, const bf16x8 (&pf)[2]) __attribute__((always_inline)) {
