@@ -1,17 +1,19 @@
-"""Build libfgg.so (the HIP kernels and the C ABI) in-tree for gfx950.
+"""Build libfgg.so (the HIP kernels and the C ABI) in-tree for gfx950, and
+_attention.so (the compiled part of the Python binding, host code only).
 
     python -m fp4_grouped_gemm_amd.build        (or fp4_grouped_gemm_amd.build.build())
 
 Every source is compiled with hipcc for gfx950 only; packed FP32 VALU
 instructions are disabled (-packed-fp32-ops) and MFMA results are kept in
 VGPRs (-amdgpu-mfma-vgpr-form).  Objects go to _build/ at the
-repository root, the shared library next to this file.
+repository root, the shared libraries next to this file.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -32,15 +34,40 @@ FLAGS = [
     "-Wall", "-Wno-unused-command-line-argument",
     "-I" + os.path.join(ROOT, "include"),
 ]
+BINDING = os.path.join(PKG, "_attention.so")
+
+
+def _run(cmd: list[str], what: str) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def build_binding() -> str:
+    """Compile _attention.so against the installed torch and link it to libfgg.so."""
+    import torch
+    home = os.path.dirname(torch.__file__)
+    tmp = BINDING + ".tmp"
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+          "-I" + os.path.join(ROOT, "include"),
+          *(flag for d in (os.path.join(home, "include"),
+                           os.path.join(home, "include", "torch", "csrc", "api", "include"),
+                           sysconfig.get_path("include"),
+                           os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"))
+            for flag in ("-isystem", d)),
+          os.path.join(CSRC, "attention_binding.cpp"), "-o", tmp,
+          "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_hip", "-lc10",
+          LIB, "-Wl,-rpath,$ORIGIN"], "attention_binding.cpp")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def _compile(src: str) -> str:
     out = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
     lang = ["-x", "hip"] if src.endswith(".cpp") else []
     cmd = [HIPCC, *FLAGS, *lang, "-c", os.path.join(CSRC, src), "-o", out]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"hipcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+    _run(cmd, f"hipcc for {src}")
     return out
 
 
@@ -70,13 +97,13 @@ def build(verbose: bool = False) -> str:
     with ThreadPoolExecutor(len(SOURCES)) as ex:
         objs = list(ex.map(_compile, SOURCES))
     tmp = LIB + ".tmp"
-    cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-Wl,-soname,libfgg.so", *objs, "-o", tmp]
+    _run(cmd, "link")
     os.replace(tmp, LIB)
+    build_binding()
     if verbose:
         print("built", LIB)
+        print("built", BINDING)
     return LIB
 
 

@@ -1,13 +1,33 @@
 """Refusals of the attention entry points: the C ABI's checks (before any
 device is touched) and the binding's."""
 import ctypes
+import struct
 
 import pytest
 
 import fp4_grouped_gemm_amd as fgg
 
 torch = pytest.importorskip("torch")
-from fp4_grouped_gemm_amd.attention import _KV_CACHE, _lib, _STRIDES  # noqa: E402
+
+_KV_CACHE = struct.Struct("@PPPPPqqqqqqqiiiiiii")  # fgg_kv_cache
+_STRIDES = struct.Struct("@6q")
+
+
+def _lib():
+    lib = fgg.load_library()
+    P, I, L, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
+    B = ctypes.c_char_p  # packed structures and arrays
+    for name, args in (
+        ("rope_kv_append", [B, P, P, P, B, P, I, I, I, P, P, P, P, I, I, P]),
+        ("paged_decode_attention_workspace", [B, I, ctypes.POINTER(ctypes.c_size_t)]),
+        ("paged_decode_attention", [B, P, L, L, P, F, P, I, P, ctypes.c_size_t, P]),
+        ("prompt_attention", [P, P, P, B, P, F, P, I, I, I, I, I, P]),
+    ):
+        fn = getattr(lib, name)
+        fn.restype = ctypes.c_int
+        fn.argtypes = args
+    return lib
+
 
 P = 0x10000  # 16-byte aligned and never dereferenced: every call below is refused
 
