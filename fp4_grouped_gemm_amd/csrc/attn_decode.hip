@@ -40,11 +40,12 @@ constexpr int kMaxHeads = 16;  // query heads of a KV head in one row of work
 // Waves of a workgroup, and workgroups on a compute unit.  Registers allow
 // three waves a SIMD: three workgroups of four waves that share the list, or
 // one of twelve that takes a whole row.  The latter needs no join and no second
-// launch; its waves take 384 tokens at once.  It is taken for tables of two
-// such steps (one row of 517 tokens: 9.1 against 8.6 us on the GPU, but 8.9
-// against 12.5 us a call with the launches), and of four where the rows fill
-// the card (256 rows of 1000 tokens 26.4 against 33.6 us, 1024 rows 100 against
-// 103 us; a single row of 1000 tokens 12.9 against 8.7 us).
+// launch; its waves take 384 tokens at once.  It is taken for tables of one such
+// step (a call on a row of 300 tokens 7.3 us, and two launches take the host 9.3),
+// of two where the rows fill half of the card (240 rows of 700 tokens 16.9 against
+// 22.2 us, 128 rows 14.9 either way; a row of 517 tokens 9.2 against 9.3, of 700
+// 11.1 against 9.3 us), and of four where they fill it (256 rows of 1000 tokens
+// 26.4 against 33.6 us, 1024 rows 100 against 103 us).
 constexpr int kListWaves = 4, kListPerCu = 3, kTile = kListWaves * kWaveTokens;
 constexpr int kWholeWaves = 12;
 constexpr int kWholeStep = kWholeWaves * kWaveTokens;
@@ -457,7 +458,8 @@ using namespace decode_detail;
 
 int decode_workgroups(int batch, int q_heads, int kv_heads, long long max_len, int num_cus) {
   const long long rows = rows_of(batch, q_heads, kv_heads);
-  if (max_len <= (rows >= num_cus ? 4 : 2) * kWholeStep) return 0;
+  const int steps = rows >= num_cus ? 4 : 2 * rows >= num_cus ? 2 : 1;
+  if (max_len <= steps * kWholeStep) return 0;
   const long long tiles = rows * ((max_len + kTile - 1) / kTile);
   const long long cap = (long long)kListPerCu * num_cus;
   return (int)(tiles < cap ? tiles : cap);

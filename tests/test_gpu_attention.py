@@ -163,6 +163,12 @@ def test_decode_table_widths(tokens):
     _check_decode(a, out, rows=[0, 1, 2, 70, 138, 139])
 
 
+@pytest.mark.parametrize("tokens", [384, 385, 768, 769])
+def test_decode_table_widths_at_half_a_card_of_rows(tokens):
+    _decode([tokens, 700, 0] + [31] * 60, 2, 2, 64, 1, seed=tokens)  # 126 rows
+    _decode([tokens, 700, 0] + [31] * 61, 2, 2, 64, 1, seed=tokens)  # 128
+
+
 def test_decode_more_rows_than_slices():
     """Rows of many more sequences than there are workgroups, some of them shared."""
     lens = [int(x) for x in np.random.default_rng(5).integers(0, 300, 420)]
