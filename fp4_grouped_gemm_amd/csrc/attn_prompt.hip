@@ -47,11 +47,12 @@ constexpr int kWaves = kThreads / 64;
 constexpr int rows_of(int KG, int HP) { return 32 * kWaves / (KG * HP); }
 constexpr float kSlack = 8.f;  // weights may reach 2^kSlack before a rescaling
 
-// sum plus the two BF16 values of a word.
+// sum plus the product of two words' BF16 values.  (Words by value: of an
+// element of a vector the compiler's bit cast takes the first one.)
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ float add_pair(uint32_t w, float sum) {
-  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), __builtin_bit_cast(bf16x2, 0x3F803F80u),
-                                         sum, false);
+constexpr uint32_t kOnes = 0x3F803F80u;
+__device__ __forceinline__ float add_pair(uint32_t x, uint32_t y, float sum) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, x), __builtin_bit_cast(bf16x2, y), sum, false);
 }
 
 // Segment i of the packed tokens: 0 is what lies before the first prompt,
@@ -65,12 +66,10 @@ __device__ __forceinline__ void segment(const PromptArgs& a, int i, int& lo, int
 // Its tiles of `rows` queries.
 __device__ __forceinline__ int row_tiles(int lo, int hi, int rows) { return (hi - lo + rows - 1) / rows; }
 
-// The two BF16 values of a word: bits 15 and 31 of odd_bits tell whether they
-// are infinite or NaN (an exponent of all ones plus one carries there, and no
-// further); without_odd puts zeros in their place.
-__device__ __forceinline__ uint32_t odd_bits(uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; }
+// A word's two BF16 values with zeros in the place of those that are infinite
+// or NaN (an exponent of all ones plus one carries into the sign's bit).
 __device__ __forceinline__ uint32_t without_odd(uint32_t w) {
-  const uint32_t odd = odd_bits(w);
+  const uint32_t odd = (w & 0x7F807F80u) + 0x00800080u;
   return w & ~((odd & 0x8000u ? 0xFFFFu : 0u) | (odd & 0x80000000u ? 0xFFFF0000u : 0u));
 }
 
@@ -313,7 +312,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void prompt_kernel(Promp
     // BF16: an instruction for two of them.
     auto weights = [&](const f32x16& s, bf16x8 (&pf)[2]) __attribute__((always_inline)) {
       const float ms = m == kNegInf ? 0.f : m * scale2;
-      float sum[2] = {0.f, 0.f};
+      float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         float p[8];
@@ -322,10 +321,13 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void prompt_kernel(Promp
         const u32x4 w = {pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]),
                          pack_bf16(p[6], p[7])};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sum[j & 1] = add_pair(w[j], sum[j & 1]);
+        for (int j = 0; j < 4; j += 2) {
+          sum0 = add_pair(w[j], kOnes, sum0);
+          sum1 = add_pair(w[j + 1], kOnes, sum1);
+        }
         pf[k] = __builtin_bit_cast(bf16x8, w);
       }
-      l += sum[0] + sum[1];
+      l += sum0 + sum1;
     };
     auto add_odd = [&](int k0) __attribute__((always_inline)) {
       for (int u = k0; u <= query; ++u) {
@@ -360,14 +362,14 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void prompt_kernel(Promp
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         u32x4 v[kBlocks];
-        uint32_t odd = 0;
+        float odd[2] = {0.f, 0.f};  // NaN, once a value is infinite or NaN (zero times it)
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i) {
           v[i] = value(block, k, i);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) odd |= odd_bits(v[i][x]);
+          for (int x = 0; x < 4; ++x) odd[x & 1] = add_pair(v[i][x], 0u, odd[x & 1]);
         }
-        if (__any((odd & 0x80008000u) != 0)) {
+        if (__any(odd[0] + odd[1] != 0.f)) {
           any = true;
 #pragma unroll
           for (int i = 0; i < kBlocks; ++i)
