@@ -13,7 +13,7 @@
 // A row that lies in one slice is finished there; the pieces of the others
 // are joined by a second kernel.  Measured: 64 sequences of 12000 to 32768
 // tokens, 16 KV heads of 64, 804 us (5.4 GB, 6.8 TB/s); 128 of 2000 to 8191, 8 KV
-// heads of 128 in E4M3, 203 us (5.7 TB/s); 96 of 1 to 6000 65 us (4.7 TB/s); one
+// heads of 128 in E4M3, 198 us (5.9 TB/s); 96 of 1 to 6000 65 us (4.7 TB/s); one
 // of 130001 on 4 KV heads 53 us (5.0 TB/s), 6 of them the join.
 //
 // A wave takes 32 tokens of a tile.  S^T = K Q^T on 16x16x32 MFMAs: the A

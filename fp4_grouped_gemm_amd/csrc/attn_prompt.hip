@@ -15,13 +15,14 @@
 // scores, maxima, sums and outputs are FP32.
 //
 // Four waves share the keys and values of a KV head through LDS, which direct
-// loads fill 64 keys ahead.  Bound by the matrix cores and the power they
-// draw: 4 D operations a query and key, and about 4.5 vector instructions
-// between two MFMAs.  Measured: 32 heads of 128, prompts of 4096 and 8192
-// tokens, 610 us, 1130 TFLOP/s, where a matrix product of 16384^3 reaches 1359;
-// MFMAs busy 62% of the cycles, at a clock of 1.75 GHz; the same without loads
-// or without softmax 566 us, without both 490 us.  Heads of 64, the same
-// prompts: 359 us, 958 TFLOP/s (half the matrix work to each exponential).
+// loads fill 64 keys ahead.  Heads of 128 are bound by the matrix cores and the
+// power they draw: 4 D operations a query and key.  Measured: 32 heads of 128,
+// prompts of 4096 and 8192 tokens, 617 us, 1113 TFLOP/s, where a matrix product
+// of 16384^3 reaches 1359; MFMAs busy 64% of the cycles, at a clock of 1.75 GHz;
+// the same without loads or without softmax 566 us, without both 490 us.  Heads
+// of 64 are bound by vector instructions: 55 plain ones and 16 exponentials (of
+// four times the cycles) to 8 MFMAs a block; the same prompts 354 us, 970
+// TFLOP/s; 24 prompts of 17 to 1501 tokens 48 us.
 //
 // A masked value must not reach the output even where it is infinite or NaN:
 // masked scores are overwritten, but in the product with V a weight of 0
