@@ -585,10 +585,18 @@ template <int D>
 hipError_t launch(const PromptArgs& a, hipStream_t s) {
   // A workgroup with 128 (head, query) rows loads a key for four waves.  Where
   // that would leave compute units without work or with one (long) item each,
-  // halves of them, split over the keys, spread better.  Measured (D = 128): 8
-  // heads of 4001 tokens 60 against 49 us, 32 heads of 1000 22 against 20 us,
-  // but 32 heads of 2048 46 against 52 us and 12288 tokens 635 against 736 us.
-  const bool split = (long long)((a.T + 127) / 128) * a.q_heads <= a.num_cus;
+  // halves of them, split over the keys, spread better: up to as many items as
+  // compute units, or twice as many of heads of 64, four of which fit on one.
+  // Measured, whole against split: 8 heads of 128, 4001 tokens 60 against 49 us, 32
+  // of 1000 22 against 20 us, but 32 of 2048 46 against 52 us; 32 heads of 64,
+  // 1500 tokens 24.3 against 20.4 us, 2048 33.2 against 31.1 us, 4096 no difference.
+  // A split costs each workgroup a join and a larger tile per prompt, so
+  // prompts have to be long for it, the longer the fuller the card is already (32
+  // heads of 128, 20 prompts of 30 tokens 7.8 against 12.1 us, 4 of 200 10.3 against
+  // 11.6 us, 2 of 400 13.0 against 12.9 us; 16 heads, 3 of 200 9.6 against 9.0 us; of
+  // 64, 4 of 500 13.1 against 13.7 us).
+  const long long items = (long long)((a.T + 127) / 128) * a.q_heads;
+  const bool split = items <= (D == 64 ? 2 : 1) * a.num_cus && items * 448 * a.batch <= (long long)a.num_cus * a.T;
   if (split) return launch<D, 2, 1>(a, s);
   // Its waves take heads of one KV head, as many of four as divide the group:
   // fewer queries then make up the rows, and less is computed for nothing on

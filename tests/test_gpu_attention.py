@@ -449,6 +449,14 @@ def test_prompt_lengths(d, lens):
     _check_prompt(a, out)
 
 
+@pytest.mark.parametrize("lens,hq,hk,d", [([1100], 32, 8, 64), ([30] * 20, 32, 8, 128), ([200] * 4, 30, 5, 128),
+                                          ([97, 0, 33], 32, 32, 64), ([900, 700], 20, 4, 64)])
+def test_prompt_long_and_short_of_many_heads(lens, hq, hk, d):
+    """Both sides of the choice between whole tiles and halves split over the keys."""
+    a, out = _prompt(lens, hq, hk, d, seed=hq)
+    _check_prompt(a, out)
+
+
 @pytest.mark.parametrize("hq,hk", [(1, 1), (7, 1), (6, 3), (16, 2), (3, 3), (40, 8)])
 def test_prompt_head_groups(hq, hk):
     for d in (64, 128):
