@@ -77,7 +77,8 @@ def prompt_attention(q, k, v, starts, *, scale=None, out=None, stream=None):
     q [T, Hq, D], k and v [T, Hkv, D]: bfloat16, any strides of multiples of 8
     with D contiguous, Hq a multiple of Hkv.  starts: int32 [B + 1],
     non-decreasing: prompt i is the tokens [starts[i], starts[i + 1]); tokens
-    of no prompt give zeros.  scale: of the scores, D ** -0.5 if None.
+    of no prompt give zeros (a start before an earlier one counts as the largest
+    of those).  scale: of the scores, D ** -0.5 if None.
     Returns bfloat16 [T, Hq, D]."""
     if stream is not None:
         with _on(stream, q):

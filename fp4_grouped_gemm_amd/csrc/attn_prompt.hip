@@ -57,12 +57,12 @@ __device__ __forceinline__ float add_pair(uint32_t x, uint32_t y, float sum) {
 }
 
 // Segment i of the packed tokens: 0 is what lies before the first prompt,
-// 1 .. batch the prompts, batch + 1 what lies after the last.  Every bound is
-// clamped to [0, T], and a segment that would end before it starts is empty.
-__device__ __forceinline__ void segment(const PromptArgs& a, int i, int& lo, int& hi) {
-  lo = i == 0 ? 0 : min(max(a.starts[i - 1], 0), a.T);
-  hi = i > a.batch ? a.T : min(max(a.starts[i], 0), a.T);
-  if (hi < lo) hi = lo;
+// 1 .. batch the prompts, batch + 1 what lies after the last.  It ends at the
+// largest of the bounds up to its own (a bound that lies before an earlier one
+// counts as that one), and there the next one begins: whatever the bounds hold,
+// the segments share out the tokens [0, T], as the grid's size assumes.
+__device__ __forceinline__ int bound(const PromptArgs& a, int i) {
+  return i > a.batch ? a.T : min(max(a.starts[i], 0), a.T);
 }
 // Its tiles of `rows` queries.
 __device__ __forceinline__ int row_tiles(int lo, int hi, int rows) { return (hi - lo + rows - 1) / rows; }
@@ -89,24 +89,26 @@ __device__ __forceinline__ void advance(i32x4& rs, long long bytes) {
   rs[1] = (int)(uint32_t)(at >> 32);
 }
 
-// Sum and maximum over a wave of values that are not negative: within rows of
-// 16 lanes, then across them (DPP row_shr 1, 2, 4, 8, row_bcast 15, 31).
+// Sum and maximum of values that are not negative over a wave's lanes up to
+// each: within rows of 16 lanes, then across them (DPP row_shr 1, 2, 4, 8,
+// row_bcast 15, 31); and over the wave.
 template <class Op>
-__device__ __forceinline__ int wave_reduce(int v, Op op) {
+__device__ __forceinline__ int wave_scan(int v, Op op) {
   v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true));
   v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true));
   v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true));
   v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true));
   v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false));
   v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false));
-  return __builtin_amdgcn_readlane(v, 63);
+  return v;
+}
+__device__ __forceinline__ int max_upto(int v) {
+  return wave_scan(v, [](int x, int y) { return max(x, y); });
 }
 __device__ __forceinline__ int wave_sum(int v) {
-  return wave_reduce(v, [](int x, int y) { return x + y; });
+  return __builtin_amdgcn_readlane(wave_scan(v, [](int x, int y) { return x + y; }), 63);
 }
-__device__ __forceinline__ int wave_max(int v) {
-  return wave_reduce(v, [](int x, int y) { return max(x, y); });
-}
+__device__ __forceinline__ int wave_max(int v) { return __builtin_amdgcn_readlane(max_upto(v), 63); }
 
 // Maximum over a lane and its partner in the other half of the wave.
 __device__ __forceinline__ float half_max(float v) {
@@ -148,11 +150,9 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void prompt_kernel(Promp
   if (segs <= 64) {
     // over all prompts: level j holds the j-th tile of each segment with more
     // than j; highest levels first.  A segment to a lane.
-    int n = 0;
-    if (lane < segs) {
-      segment(a, lane, lo, hi);
-      n = row_tiles(lo, hi, kRows);
-    }
+    lo = max_upto(lane > 0 && lane < segs ? bound(a, lane - 1) : 0);
+    hi = lane < segs ? max(lo, bound(a, lane)) : lo;
+    const int n = row_tiles(lo, hi, kRows);
     auto from_level = [&](int j) { return wave_sum(max(n - j, 0)); };  // tiles at level j and above
     if (item >= from_level(0)) return;
     int below = 0, above = wave_max(n);  // from_level(below) > item >= from_level(above)
@@ -177,10 +177,24 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void prompt_kernel(Promp
     // prompt by prompt; several to a lane
     const int chunk = (segs + 63) / 64;
     const int i0 = min(lane * chunk, segs), i1 = min(i0 + chunk, segs);
-    int sum = 0;
-    for (int i = i0; i < i1; ++i) {
-      segment(a, i, lo, hi);
-      sum += row_tiles(lo, hi, kRows);
+    // tiles of the lane's segments if the first one begins at `from`, and the
+    // last one's end
+    auto tiles_from = [&](int from, int& end) {
+      int sum = 0;
+      end = from;
+      for (int i = i0; i < i1; ++i) {
+        const int to = max(end, bound(a, i));
+        sum += row_tiles(end, to, kRows);
+        end = to;
+      }
+      return sum;
+    };
+    int from = i0 > 0 ? bound(a, i0 - 1) : 0, end;
+    int sum = tiles_from(from, end);
+    const int earlier = __shfl_up(max_upto(end), 1, 64);
+    if (lane > 0 && earlier > from) {  // only where bounds decrease
+      from = earlier;
+      sum = tiles_from(from, end);
     }
     int upto = sum;
 #pragma unroll
@@ -192,11 +206,13 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void prompt_kernel(Promp
     if (past == 0) return;
     const int src = __builtin_ctzll(past);
     int before = __builtin_amdgcn_readlane(upto - sum, src), n;
+    lo = __builtin_amdgcn_readlane(from, src);
     for (seg = src * chunk;; ++seg) {
-      segment(a, seg, lo, hi);
+      hi = max(lo, bound(a, seg));
       n = row_tiles(lo, hi, kRows);
       if (item < before + n) break;
       before += n;
+      lo = hi;
     }
     tile = n - 1 - (item - before);
   }

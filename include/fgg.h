@@ -535,7 +535,8 @@ fgg_status paged_decode_attention(const fgg_kv_cache* cache, const void* q, long
  *            token, k head, v token, v head} in values (multiples of 8)
  *   starts   [batch + 1] int32, non-decreasing: prompt i is tokens
  *            [starts[i], starts[i + 1]) (clamped to [0, T]); read on the
- *            device only.  Tokens of no prompt get zeros.
+ *            device only.  Tokens of no prompt get zeros.  A start that lies
+ *            before an earlier one counts as the largest of those.
  *   out      BF16 [T, q_heads, head_dim]
  *
  * Scores, maxima, sums and outputs are FP32; the weights are rounded to BF16

@@ -99,12 +99,14 @@ def paged_decode_attention(q, k_cache, v_cache, table, lengths, scale, k_scale=N
 
 
 def prompt_attention(q, k, v, starts, scale):
-    """q [T, Hq, D], k and v [T, Hkv, D] -> (out, sums of |v|)."""
+    """q [T, Hq, D], k and v [T, Hkv, D] -> (out, sums of |v|).  A start that lies
+    before an earlier one counts as the largest of those."""
     T, hq, d = q.shape
     hk = k.shape[1]
     out, mag = np.zeros(q.shape), np.zeros(q.shape)
+    starts = np.maximum.accumulate(np.clip(np.asarray(starts, np.int64), 0, T))
     for i in range(len(starts) - 1):
-        lo, hi = (min(max(int(x), 0), T) for x in starts[i:i + 2])
+        lo, hi = int(starts[i]), int(starts[i + 1])
         for t in range(lo, hi):
             for h in range(hq):
                 kvh = h // (hq // hk)

@@ -1,0 +1,82 @@
+"""GPU tests of the attention operators where inputs are at the edge of what the
+entry points define: bounds in any order, tables and batches of the largest
+sizes, strides of dimensions that hold one entry.  Tolerances as in
+test_gpu_attention.py."""
+import numpy as np
+import pytest
+
+import fp4_grouped_gemm_amd as fgg
+from tests.gpu_util import log
+from tests.test_gpu_attention import _bf16, _check_prompt, _int, _prompt
+
+pytestmark = pytest.mark.gpu
+
+
+def _torch():
+    import torch
+    return torch
+
+
+# --------------------------------------------------- prompts: bounds in any order
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hk", [(4, 1), (8, 4), (2, 2), (64, 8)])
+@pytest.mark.parametrize("starts", [[0, 200, 0, 200], [0, 200, 0, 200, 0, 200, 3], [150, 20, 160, 90, 140, 190],
+                                    [-7, 120, 119, 1 << 30, 5], [200, 0], [60, 61, 60, 200, 100]])
+def test_prompt_starts_that_decrease(starts, hq, hk, d):
+    """Prompts never overlap and every row is written, whatever the bounds hold."""
+    torch = _torch()
+    rng = np.random.default_rng(len(starts) + d)
+    q, k, v = _bf16(rng, 200, hq, d), _bf16(rng, 200, hk, d), _bf16(rng, 200, hk, d)
+    out = torch.full_like(q, float("nan"))
+    log(f"prompt starts={starts} hq={hq} hk={hk} d={d}")
+    fgg.prompt_attention(q, k, v, _int(starts), out=out)
+    if hq <= 8:
+        _check_prompt(dict(q=q, k=k, v=v, starts=_int(starts), scale=None), out, str(starts))
+    sorted_ = np.maximum.accumulate(np.clip(starts, 0, 200))
+    assert torch.equal(out, fgg.prompt_attention(q, k, v, _int(sorted_)))
+
+
+@pytest.mark.parametrize("batch", [61, 62, 63, 64, 200, 700])
+@pytest.mark.parametrize("hq,hk", [(8, 2), (4, 2), (2, 2)])
+def test_prompt_starts_in_no_order(batch, hq, hk):
+    """Of many prompts, on both sides of the number up to which a lane of the
+    search holds one of them."""
+    torch = _torch()
+    rng = np.random.default_rng(batch)
+    T = 1000
+    q, k, v = _bf16(rng, T, hq, 64), _bf16(rng, T, hk, 64), _bf16(rng, T, hk, 64)
+    for which in range(3):
+        starts = np.sort(rng.integers(-50, T + 50, batch + 1))
+        if which == 1:  # a few out of order
+            at = rng.integers(0, batch + 1, 5)
+            starts[at] = rng.integers(0, T, 5)
+        if which == 2:
+            starts = rng.permutation(starts) // 2
+        out = torch.full_like(q, float("nan"))
+        log(f"prompt {batch} starts in order {which} hq={hq}")
+        fgg.prompt_attention(q, k, v, _int(starts), out=out)
+        _check_prompt(dict(q=q, k=k, v=v, starts=_int(starts), scale=None), out, f"order {which}")
+
+
+def test_prompt_replay_with_starts_that_decrease():
+    """A captured call whose bounds turn bad, and good again."""
+    torch = _torch()
+    a, _ = _prompt([200, 56], 4, 2, 128, seed=6)
+    out = torch.empty_like(a["q"])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        fgg.prompt_attention(**a, out=out)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    log("prompt graph, bounds that decrease")
+    with torch.cuda.graph(g):
+        fgg.prompt_attention(**a, out=out)
+    for starts in ([256, 0, 256], [0, 256, 0], [0, 200, 256]):
+        a["starts"].copy_(_int(starts))
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        _check_prompt(a, out, f"replay {starts}")
