@@ -28,13 +28,17 @@
 // for 128 sequences of 2000 to 8191 tokens in E4M3) and takes the weights'
 // rounding out of the result.  Scores, maxima, sums and outputs are FP32.
 #include "attn.h"
+#include "attn_list.h"
 
 namespace fgg {
 namespace decode_detail {
 
 using namespace attn;
 
-constexpr int kWaveTokens = 32;
+using attn_list::kTile;
+using attn_list::kWaveTokens;
+using attn_list::tiles_of;
+
 constexpr int kMaxHeads = 16;  // query heads of a KV head in one row of work
 
 // Waves of a workgroup, and workgroups on a compute unit.  Registers allow
@@ -46,7 +50,7 @@ constexpr int kMaxHeads = 16;  // query heads of a KV head in one row of work
 // 22.2 us, 128 rows 14.9 either way; a row of 517 tokens 9.2 against 9.3, of 700
 // 11.1 against 9.3 us), and of four where they fill it (256 rows of 1000 tokens
 // 26.4 against 33.6 us, 1024 rows 100 against 103 us).
-constexpr int kListWaves = 4, kListPerCu = 3, kTile = kListWaves * kWaveTokens;
+constexpr int kListWaves = attn_list::kWaves, kListPerCu = 3;
 constexpr int kWholeWaves = 12;
 constexpr int kWholeStep = kWholeWaves * kWaveTokens;
 
@@ -55,21 +59,6 @@ __device__ __forceinline__ int length_of(const DecodeArgs& a, int b) {
   const int n = a.lengths[b];
   return n < 0 ? 0 : n > cap ? (int)cap : n;
 }
-// An empty row has a tile too: the one that writes its zeros.
-__device__ __forceinline__ int tiles_of(int len) { return len ? (len + kTile - 1) / kTile : 1; }
-
-// The list in slices that differ by at most one tile, none of them empty (a
-// row's pieces come from consecutive slices): where one begins, and which one
-// holds a tile.  Workgroups past the last slice have nothing to do.
-__device__ __forceinline__ int slices_of(int total) { return min((int)gridDim.x, total); }
-__device__ __forceinline__ int slice_start(int i, int total) {
-  const int n = slices_of(total);
-  return i < n ? (int)((long long)i * total / n) : total;
-}
-__device__ __forceinline__ int slice_of(int tile, int total) {
-  return (int)(((long long)(tile + 1) * slices_of(total) - 1) / total);
-}
-
 // Rows of work of a KV head: its query heads by kMaxHeads.
 __device__ __forceinline__ int head_groups(const DecodeArgs& a) {
   return (a.q_heads / a.c.kv_heads + kMaxHeads - 1) / kMaxHeads;
@@ -135,7 +124,7 @@ __global__ __launch_bounds__(kWaves * 64, kWhole ? kWaves / 4 : kListPerCu) void
       if (lane >= off) upto += u;
     }
     total = __builtin_amdgcn_readlane(upto, 63) * rows;
-    pos = slice_start(blockIdx.x, total);
+    pos = attn_list::slice_start(blockIdx.x, total, gridDim.x);
     const int first = min(pos, total - 1);
     // the lane whose sequences hold tile `first`, then the sequence
     const int src = __builtin_ctzll(__ballot(first < upto * rows));
@@ -145,7 +134,7 @@ __global__ __launch_bounds__(kWaves * 64, kWhole ? kWaves / 4 : kListPerCu) void
       if (first < (before + n) * rows) break;
       before += n;
     }
-    end = slice_start(blockIdx.x + 1, total);
+    end = attn_list::slice_start(blockIdx.x + 1, total, gridDim.x);
     by_row = joins_by_row(a.c.batch * rows, (int)gridDim.x);
     if (!by_row && tid == 0) a.split[blockIdx.x].first = -1;
   }
@@ -184,7 +173,7 @@ __global__ __launch_bounds__(kWaves * 64, kWhole ? kWaves / 4 : kListPerCu) void
     float m = kNegInf, l = 0.f;
 
     for (int t = t0; t < t1; ++t) {
-      const int tok0 = t * kStep + wave * kWaveTokens;
+      const int tok0 = attn_list::first_token(t, kStep, wave);
       if (tok0 >= len) break;
       // lane L looks up token tok0 + L % 32: its page, or -1
       const int tok = tok0 + (lane & 31);
@@ -308,7 +297,7 @@ __global__ __launch_bounds__(kWaves * 64, kWhole ? kWaves / 4 : kListPerCu) void
     if (!kWhole && t0 == 0 && tid == 0) {
       if (!whole)
         a.split[by_row ? b * rows + row : (int)blockIdx.x] =
-            SplitRow{(int)blockIdx.x, slice_of(pos + n - 1, total), b, head0, heads, {}};
+            SplitRow{(int)blockIdx.x, attn_list::slice_of(pos + n - 1, total, gridDim.x), b, head0, heads, {}};
       else if (by_row)
         a.split[b * rows + row].first = -1;
     }

@@ -1,7 +1,14 @@
 """Host tests of the attention operators' definitions at the edges."""
+import os
+import shutil
+import subprocess
+
 import numpy as np
+import pytest
 
 from oracle import attention as oa
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def test_a_start_before_an_earlier_one_counts_as_that_one():
@@ -12,3 +19,14 @@ def test_a_start_before_an_earlier_one_counts_as_that_one():
             assert np.array_equal(got, want)
     out, _ = oa.prompt_attention(q, k, v, [3, 7, 5, 8], 0.5)
     assert not out[:3].any() and not out[8:].any() and out[3:8].all()
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_the_list_of_work_at_the_ends_of_its_range(tmp_path):
+    """csrc/attn_list.h, the arithmetic the kernels call: tests/attn_list_check.cpp.
+    (Overflows trap instead of wrapping.)"""
+    exe = str(tmp_path / "attn_list_check")
+    subprocess.run(["g++", "-O1", "-std=c++17", "-Wall", "-ftrapv", "-I", os.path.join(ROOT, "fp4_grouped_gemm_amd", "csrc"),
+                    os.path.join(ROOT, "tests", "attn_list_check.cpp"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and " 0 failed" in r.stdout, (r.returncode, r.stdout)

@@ -7,7 +7,7 @@ import pytest
 
 import fp4_grouped_gemm_amd as fgg
 from tests.gpu_util import log
-from tests.test_gpu_attention import _bf16, _check_prompt, _int, _prompt
+from tests.test_gpu_attention import _bf16, _check_decode, _check_prompt, _int, _prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +80,27 @@ def test_prompt_replay_with_starts_that_decrease():
         g.replay()
         torch.cuda.synchronize()
         _check_prompt(a, out, f"replay {starts}")
+
+
+# ------------------------------------------------------------ decode: largest sizes
+@pytest.mark.parametrize("length", [(1 << 31) - 1, (1 << 31) - 64, (1 << 31) - 127, (1 << 31) - 128, (1 << 31) - 200])
+def test_decode_table_of_2_31_tokens(length):
+    """Lengths up to the end of a table of 2^31 - 64 tokens that has pages only at
+    its start, across its middle and at its end."""
+    torch = _torch()
+    rng = np.random.default_rng(1)
+    page, width, d = 64, (1 << 25) - 1, 64
+    pages = {0: 3, (1 << 24) - 1: 1, 1 << 24: 0, width - 3: 5, width - 2: 2, width - 1: 4}
+    table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    for col, p in pages.items():
+        table[0, col] = p
+    k, v = _bf16(rng, 6, 1, page, d), _bf16(rng, 6, 1, page, d)
+    q = _bf16(rng, 1, 2, d)
+    log(f"decode, a table of 2^31 - 64 tokens, length {length}")
+    out = fgg.paged_decode_attention(q, k, v, table, _int([length]))
+    # the same tokens under a short table
+    n = min(length, page * width)
+    tokens = sum(max(0, min(page, n - col * page)) for col in pages)
+    short = dict(q=q, k_cache=k, v_cache=v, page_table=_int([list(pages.values())]), lengths=_int([tokens]), scale=None,
+                 k_scale=None, v_scale=None)
+    _check_decode(short, out)
