@@ -448,7 +448,8 @@ using namespace decode_detail;
 int decode_workgroups(int batch, int q_heads, int kv_heads, long long max_len, int num_cus) {
   const long long rows = rows_of(batch, q_heads, kv_heads);
   const int steps = rows >= num_cus ? 4 : 2 * rows >= num_cus ? 2 : 1;
-  if (max_len <= steps * kWholeStep) return 0;
+  // (a launch takes fewer than 2^32 threads)
+  if (max_len <= steps * kWholeStep && rows * (kWholeWaves * 64) <= 0xFFFFFFFFLL) return 0;
   const long long tiles = rows * ((max_len + kTile - 1) / kTile);
   const long long cap = (long long)kListPerCu * num_cus;
   return (int)(tiles < cap ? tiles : cap);

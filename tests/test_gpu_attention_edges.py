@@ -104,3 +104,21 @@ def test_decode_table_of_2_31_tokens(length):
     short = dict(q=q, k_cache=k, v_cache=v, page_table=_int([list(pages.values())]), lengths=_int([tokens]), scale=None,
                  k_scale=None, v_scale=None)
     _check_decode(short, out)
+
+
+def test_decode_more_rows_than_one_launch_takes():
+    """A million short sequences of eight KV heads: a workgroup of 768 threads for
+    each row would pass the 2^32 threads of a launch."""
+    torch = _torch()
+    batch, heads, d, pages = 1 << 20, 8, 64, 16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    k, v = (torch.randn((pages, heads, 1, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((batch, heads, d), generator=g, device="cuda", dtype=torch.bfloat16)
+    table = torch.randint(0, pages, (batch, 1), generator=g, device="cuda", dtype=torch.int32)
+    lens = torch.randint(0, 2, (batch,), generator=g, device="cuda", dtype=torch.int32)
+    log("decode, 2^20 sequences x 8 heads")
+    out = fgg.paged_decode_attention(q, k, v, table, lens)
+    # one token's weight is 1: its value as it is
+    want = torch.where(lens[:, None, None] > 0, v[table[:, 0].long(), :, 0], torch.zeros((), dtype=v.dtype, device="cuda"))
+    assert torch.equal(out, want)
