@@ -957,6 +957,10 @@ fgg_status prompt_attention(const void* q, const void* k, const void* v, const l
   if (!aligned(starts, 4)) return fail(FGG_EALIGN, fn, "starts must be 4-byte aligned");
   if (((long long)T / 32 + batch + 2) * q_heads > 0x7FFFFFFFLL)
     return fail(FGG_EUNSUPPORTED, fn, "requires (T / 32 + batch + 2) * q_heads < 2^31");
+  const long long workgroups = fgg::prompt_workgroups(T, batch, q_heads, kv_heads);
+  if (workgroups >= 1 << 24)  // a launch takes fewer than 2^32 threads
+    return fail(FGG_EUNSUPPORTED, fn, "T=%d tokens in %d prompts take %lld workgroups, a launch at most 2^24 - 1", T,
+                batch, workgroups);
   const DeviceFacts* d = current_device(fn, &st);
   if (!d) return st;
   const fgg::PromptArgs a{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),

@@ -81,6 +81,10 @@ int decode_workgroups(int batch, int q_heads, int kv_heads, long long max_len, i
 // Bytes of its workspace (part_o, part_ml, split) for that many workgroups.
 size_t decode_workspace(int workgroups, int D);
 
+// Workgroups, of 256 threads, that a prompt launch takes at most.  (Split over the
+// keys it takes up to twice as many, but that is done for few workgroups only.)
+long long prompt_workgroups(int T, int batch, int q_heads, int kv_heads);
+
 hipError_t launch_append(const AppendArgs& a, hipStream_t s);
 hipError_t launch_decode(const DecodeArgs& a, int workgroups, hipStream_t s);
 hipError_t launch_prompt(const PromptArgs& a, hipStream_t s);

@@ -588,13 +588,30 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void prompt_kernel(Promp
 
 using namespace prompt_detail;
 
+// Workgroups of a launch: at most one partly filled tile a segment.
+static long long grid_of(int T, int batch, int q_heads, int KG, int HP) {
+  return ((long long)T / rows_of(KG, HP) + batch + 2) * (q_heads / HP);
+}
+
 template <int D, int KG, int HP>
 hipError_t launch(const PromptArgs& a, hipStream_t s) {
-  // at most one partly filled tile a segment
-  const long long grid = ((long long)a.T / rows_of(KG, HP) + a.batch + 2) * (a.q_heads / HP);
-  if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;  // the host checks
-  hipLaunchKernelGGL((prompt_kernel<D, KG, HP>), dim3((unsigned)grid), dim3(kThreads), 0, s, a);
+  const unsigned grid = (unsigned)grid_of(a.T, a.batch, a.q_heads, KG, HP);  // (the host checks)
+  hipLaunchKernelGGL((prompt_kernel<D, KG, HP>), dim3(grid), dim3(kThreads), 0, s, a);
   return hipGetLastError();
+}
+
+// Heads of one KV head that the waves of a workgroup take, where the keys are not
+// split: as many of four as divide the group.  Fewer queries then make up the
+// rows, and less is computed for nothing on the diagonal (24 prompts of 17 to
+// 1501 tokens, D = 64: 54 against 59 us; nothing gained on 8192 tokens, nor where
+// the keys are split).
+static int heads_together(int q_heads, int kv_heads) {
+  const int group = q_heads / kv_heads;
+  return group % 4 == 0 ? 4 : group % 2 == 0 ? 2 : 1;
+}
+
+long long prompt_workgroups(int T, int batch, int q_heads, int kv_heads) {
+  return grid_of(T, batch, q_heads, 1, heads_together(q_heads, kv_heads));
 }
 
 template <int D>
@@ -614,13 +631,11 @@ hipError_t launch(const PromptArgs& a, hipStream_t s) {
   const long long items = (long long)((a.T + 127) / 128) * a.q_heads;
   const bool split = items <= (D == 64 ? 2 : 1) * a.num_cus && items * 448 * a.batch <= (long long)a.num_cus * a.T;
   if (split) return launch<D, 2, 1>(a, s);
-  // Its waves take heads of one KV head, as many of four as divide the group:
-  // fewer queries then make up the rows, and less is computed for nothing on
-  // the diagonal (24 prompts of 17 to 1501 tokens, D = 64: 54 against 59 us;
-  // nothing gained on 8192 tokens, nor where the keys are split).
-  const int group = a.q_heads / a.kv_heads;
-  if (group % 4 == 0) return launch<D, 1, 4>(a, s);
-  return group % 2 == 0 ? launch<D, 1, 2>(a, s) : launch<D, 1, 1>(a, s);
+  switch (heads_together(a.q_heads, a.kv_heads)) {
+    case 4: return launch<D, 1, 4>(a, s);
+    case 2: return launch<D, 1, 2>(a, s);
+    default: return launch<D, 1, 1>(a, s);
+  }
 }
 
 hipError_t launch_prompt(const PromptArgs& a, hipStream_t s) {

@@ -539,6 +539,10 @@ fgg_status paged_decode_attention(const fgg_kv_cache* cache, const void* q, long
  *            before an earlier one counts as the largest of those.
  *   out      BF16 [T, q_heads, head_dim]
  *
+ * T <= 2^24, batch <= 2^20, token strides of k and v at most 2^22 values, and
+ * (c T / 128 + batch + 2) q_heads / c < 2^24, c the largest of 4, 2, 1 that
+ * divides q_heads / kv_heads (else FGG_EINVAL or FGG_EUNSUPPORTED).
+ *
  * Scores, maxima, sums and outputs are FP32; the weights are rounded to BF16
  * for the product with V.  Keys and values that a query does
  * not attend to never reach its output, infinities and NaN included.

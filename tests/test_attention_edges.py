@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 
 from oracle import attention as oa
+from tests.test_attention_abi import _prompt
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -30,3 +31,11 @@ def test_the_list_of_work_at_the_ends_of_its_range(tmp_path):
                     os.path.join(ROOT, "tests", "attn_list_check.cpp"), "-o", exe], check=True)
     r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and " 0 failed" in r.stdout, (r.returncode, r.stdout)
+
+
+@pytest.mark.parametrize("T,batch,hq,hk", [(1000, 1 << 20, 64, 16), (100, (1 << 19) - 2 - 1, 64, 32), (128, (1 << 18) - 3, 64, 64),
+                                           (1 << 24, 1, 128, 32)])
+def test_prompts_that_one_launch_cannot_take_are_refused(T, batch, hq, hk):
+    """At 2^24 workgroups of 256 threads (2^32) and above, before any device is touched."""
+    status, msg = _prompt(T=T, batch=batch, hq=hq, hk=hk)
+    assert status == 2 and msg.startswith("prompt_attention:") and "2^24" in msg
