@@ -39,3 +39,11 @@ def test_prompts_that_one_launch_cannot_take_are_refused(T, batch, hq, hk):
     """At 2^24 workgroups of 256 threads (2^32) and above, before any device is touched."""
     status, msg = _prompt(T=T, batch=batch, hq=hq, hk=hk)
     assert status == 2 and msg.startswith("prompt_attention:") and "2^24" in msg
+
+
+@pytest.mark.parametrize("which", [2, 4])
+def test_prompt_token_strides_past_32_bit_offsets_are_refused(which):
+    strides = [1024, 128, 512, 128, 512, 128]
+    strides[which] = (1 << 22) + 8
+    status, msg = _prompt(strides=strides)
+    assert status == 2 and "token strides" in msg

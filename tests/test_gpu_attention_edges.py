@@ -122,3 +122,18 @@ def test_decode_more_rows_than_one_launch_takes():
     # one token's weight is 1: its value as it is
     want = torch.where(lens[:, None, None] > 0, v[table[:, 0].long(), :, 0], torch.zeros((), dtype=v.dtype, device="cuda"))
     assert torch.equal(out, want)
+
+
+# ------------------------------------------------------------------------ strides
+def test_prompt_heads_first_of_a_long_prompt():
+    """Keys and values of 33000 tokens stored head by head: heads lie further apart
+    than tokens may."""
+    torch = _torch()
+    rng = np.random.default_rng(3)
+    T, hq, hk, d = 33000, 4, 2, 128
+    q, k, v = _bf16(rng, T, hq, d), _bf16(rng, T, hk, d), _bf16(rng, T, hk, d)
+    starts = _int([0, 300, 32000, T])
+    kt, vt = (x.transpose(0, 1).contiguous().transpose(0, 1) for x in (k, v))
+    assert kt.stride(1) > 1 << 22
+    log("prompt, heads first, 33000 tokens")
+    assert torch.equal(fgg.prompt_attention(q, kt, vt, starts), fgg.prompt_attention(q, k, v, starts))
