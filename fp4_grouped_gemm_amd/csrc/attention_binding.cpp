@@ -50,6 +50,9 @@ const Tensor& heads(PyObject* o, const char* name) {
   return t;
 }
 
+// Stride of a dimension; one that holds a single entry may have any.
+long long step(const Tensor& t, int dim) { return t.size(dim) > 1 ? t.stride(dim) : 0; }
+
 // A contiguous vector of n values on q's device; any length if n is negative.
 template <class T>
 const T* vector(PyObject* o, const char* name, int64_t n, at::ScalarType dtype, const Tensor& q) {
@@ -98,10 +101,10 @@ fgg_kv_cache cache(PyObject* k_, PyObject* v_, PyObject* table_, PyObject* k_sca
   c.k_scale = k_scale == Py_None ? nullptr : vector<float>(k_scale, "k_scale", k.size(1), at::kFloat, q);
   c.v_scale = v_scale == Py_None ? nullptr : vector<float>(v_scale, "v_scale", k.size(1), at::kFloat, q);
   c.page_table = static_cast<const int32_t*>(table.const_data_ptr());
-  c.table_stride = table.stride(0);
+  c.table_stride = step(table, 0);
   for (int i = 0; i < 3; ++i) {
-    c.k_strides[i] = k.stride(i);
-    c.v_strides[i] = v.stride(i);
+    c.k_strides[i] = step(k, i);
+    c.v_strides[i] = step(v, i);
   }
   c.dtype = fp8 ? FGG_KV_E4M3 : FGG_KV_BF16;
   c.num_pages = (int)k.size(0);
@@ -185,7 +188,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor res = result(a[13], q, T, hq, d), k_out;
   if (return_k) k_out = at::empty({T, hk, d}, q.options());
   if (T) {
-    const long long strides[6] = {q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1)};
+    const long long strides[6] = {step(q, 0), step(q, 1), step(k, 0), step(k, 1), step(v, 0), step(v, 1)};
     const int num = as_int(turns.size(0), "cos_sin"), rot = as_int(turns.size(1), "cos_sin");
     const int tokens = as_int(T, "T"), q_heads = as_int(hq, "Hq"), interleaved = truth(a[9]);
     void* const stream = stream_on(q);
@@ -223,7 +226,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor work = need ? at::empty({(int64_t)need}, q.options().dtype(at::kByte)) : res;
     void* const stream = stream_on(q);
     call([&] {
-      return paged_decode_attention(&c, q.const_data_ptr(), q.stride(0), q.stride(1), lens, scale, res.data_ptr(),
+      return paged_decode_attention(&c, q.const_data_ptr(), step(q, 0), step(q, 1), lens, scale, res.data_ptr(),
                                     q_heads, work.data_ptr(), need, stream);
     });
   }
@@ -249,7 +252,7 @@ PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const float scale = scale_of(a[4], d);
   Tensor res = result(a[5], q, T, hq, d);
   if (T) {
-    const long long strides[6] = {q.stride(0), q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1)};
+    const long long strides[6] = {step(q, 0), step(q, 1), step(k, 0), step(k, 1), step(v, 0), step(v, 1)};
     const int tokens = as_int(T, "T"), prompts = as_int(batch, "B"), q_heads = as_int(hq, "Hq"),
               kv_heads = as_int(hk, "Hkv"), dim = as_int(d, "D");
     void* const stream = stream_on(q);

@@ -137,3 +137,29 @@ def test_prompt_heads_first_of_a_long_prompt():
     assert kt.stride(1) > 1 << 22
     log("prompt, heads first, 33000 tokens")
     assert torch.equal(fgg.prompt_attention(q, kt, vt, starts), fgg.prompt_attention(q, k, v, starts))
+
+
+def _loose(x):
+    """x with an odd stride in each dimension but the last that holds one entry."""
+    return x.as_strided(x.shape, [7 if n == 1 else s for n, s in zip(x.shape[:-1], x.stride()[:-1])] + [1])
+
+
+def test_strides_of_single_entries_do_not_matter():
+    """One token, one head, one page: the stride of such a dimension is never used."""
+    torch = _torch()
+    rng = np.random.default_rng(4)
+    q, k, v = _bf16(rng, 1, 1, 64), _bf16(rng, 1, 1, 64), _bf16(rng, 1, 1, 64)
+    log("strides of single entries")
+    assert torch.equal(fgg.prompt_attention(_loose(q), _loose(k), _loose(v), _int([0, 1])), v)
+    turns = torch.tensor([[1.0] * 8 + [0.0] * 8], device="cuda")
+    kc, vc = (torch.zeros((1, 1, 1, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = _int([[0]])
+    got = fgg.rope_kv_append(_loose(q), _loose(k), _loose(v), turns, _int([0]), _loose(table), _loose(kc), _loose(vc))
+    assert torch.equal(got, q) and torch.equal(kc[0, :, 0], k[0]) and torch.equal(vc[0, :, 0], v[0])
+    assert torch.equal(fgg.paged_decode_attention(_loose(q), _loose(kc), _loose(vc), _loose(table), _int([1])), v)
+    # one KV head among many tokens, its dimension moved into place
+    k, v, q = _bf16(rng, 50, 64), _bf16(rng, 50, 64), _bf16(rng, 50, 4, 64)
+    moved = [x[:, :, None].transpose(1, 2) for x in (k, v)]
+    assert moved[0].stride(1) == 1
+    assert torch.equal(fgg.prompt_attention(q, *moved, _int([0, 20, 50])),
+                       fgg.prompt_attention(q, k.view(50, 1, 64), v.view(50, 1, 64), _int([0, 20, 50])))
