@@ -16,6 +16,8 @@ from __future__ import annotations
 import ctypes
 import os
 
+from .attention import paged_decode_attention, prompt_attention, rope_kv_append
+
 __all__ = [
     "grouped_fp8_gemm", "fp4_gemm", "grouped_fp4_gemm", "quantize_fp8_1x128",
     "quantize_nvfp4", "grouped_fp8_gemm_tune", "fp4_gemm_tune", "grouped_fp4_gemm_tune",
@@ -71,16 +73,6 @@ class _Fp8Problem(ctypes.Structure):
 class _Options(ctypes.Structure):
     _fields_ = [("tile_id", ctypes.c_int), ("max_workgroups", ctypes.c_int),
                 ("run_split", ctypes.c_int), ("run_align", ctypes.c_int)]
-
-
-def __getattr__(name):
-    # the attention entry points live in a module that imports torch, which
-    # the C-ABI checks do without
-    if name in ("rope_kv_append", "paged_decode_attention", "prompt_attention"):
-        from . import attention
-        globals()[name] = getattr(attention, name)
-        return globals()[name]
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def load_library():

@@ -12,18 +12,27 @@ their contents change.
 """
 from __future__ import annotations
 
-import torch
+_C = None
 
-try:
-    from . import _attention as _C
-except ImportError as e:
-    raise ImportError("the attention binding is missing or was built for another torch: build it with "
-                      "`python -m fp4_grouped_gemm_amd.build`") from e
+
+def _binding():
+    """The compiled module, loaded by the first call: importing the package needs
+    neither torch nor a built library."""
+    global _C
+    import torch  # noqa: F401  (its libraries come first)
+    try:
+        from . import _attention
+    except ImportError as e:
+        raise ImportError("the attention binding is missing or was built for another torch: build it with "
+                          "`python -m fp4_grouped_gemm_amd.build`") from e
+    _C = _attention
+    return _C
 
 
 def _on(stream, q):
     """A context in which `stream` is the current one, so that memory allocated
     for the call belongs to the stream that uses it."""
+    import torch
     if stream.device != q.device:
         raise ValueError(f"stream is on {stream.device}, expected {q.device}")
     return torch.cuda.stream(stream)
@@ -52,8 +61,8 @@ def rope_kv_append(q, k, v, cos_sin, positions, page_table, k_cache, v_cache, *,
             return rope_kv_append(q, k, v, cos_sin, positions, page_table, k_cache, v_cache,
                                   seq_ids=seq_ids, interleaved=interleaved, k_scale=k_scale,
                                   v_scale=v_scale, return_k=return_k, out=out)
-    return _C.rope_kv_append(q, k, v, cos_sin, positions, page_table, k_cache, v_cache, seq_ids,
-                             interleaved, k_scale, v_scale, return_k, out)
+    return (_C or _binding()).rope_kv_append(q, k, v, cos_sin, positions, page_table, k_cache, v_cache,
+                                             seq_ids, interleaved, k_scale, v_scale, return_k, out)
 
 
 def paged_decode_attention(q, k_cache, v_cache, page_table, lengths, *, scale=None, k_scale=None,
@@ -68,7 +77,8 @@ def paged_decode_attention(q, k_cache, v_cache, page_table, lengths, *, scale=No
         with _on(stream, q):
             return paged_decode_attention(q, k_cache, v_cache, page_table, lengths, scale=scale,
                                           k_scale=k_scale, v_scale=v_scale, out=out)
-    return _C.paged_decode_attention(q, k_cache, v_cache, page_table, lengths, scale, k_scale, v_scale, out)
+    return (_C or _binding()).paged_decode_attention(q, k_cache, v_cache, page_table, lengths, scale,
+                                                     k_scale, v_scale, out)
 
 
 def prompt_attention(q, k, v, starts, *, scale=None, out=None, stream=None):
@@ -83,4 +93,4 @@ def prompt_attention(q, k, v, starts, *, scale=None, out=None, stream=None):
     if stream is not None:
         with _on(stream, q):
             return prompt_attention(q, k, v, starts, scale=scale, out=out)
-    return _C.prompt_attention(q, k, v, starts, scale, out)
+    return (_C or _binding()).prompt_attention(q, k, v, starts, scale, out)

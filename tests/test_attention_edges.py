@@ -2,6 +2,7 @@
 import os
 import shutil
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -47,3 +48,21 @@ def test_prompt_token_strides_past_32_bit_offsets_are_refused(which):
     strides[which] = (1 << 22) + 8
     status, msg = _prompt(strides=strides)
     assert status == 2 and "token strides" in msg
+
+
+@pytest.mark.parametrize("missing", ["torch", "fp4_grouped_gemm_amd._attention"])
+def test_the_package_imports_without_torch_or_the_compiled_binding(missing):
+    """What they are needed for says so when it is called."""
+    code = (f"import sys; sys.modules[{missing!r}] = None\n"
+            "from fp4_grouped_gemm_amd import *\n"
+            "import fp4_grouped_gemm_amd as fgg\n"
+            "assert all(callable(f) for f in (grouped_fp8_gemm, rope_kv_append, prompt_attention))\n"
+            "load_library()\n"
+            "try:\n"
+            "    prompt_attention(None, None, None, None)\n"
+            "except ImportError as e:\n"
+            "    print('refused:', e)\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "refused:" in r.stdout, r.stderr
+    if missing != "torch":
+        assert "python -m fp4_grouped_gemm_amd.build" in r.stdout
