@@ -1,5 +1,6 @@
 """Build libfgg.so (the HIP kernels and the C ABI) in-tree for gfx950, and
-_attention.so (the compiled part of the Python binding, host code only).
+_attention.so (the compiled part of the Python binding, host code only; it
+takes torch's headers, and is left out where there is no torch).
 
     python -m fp4_grouped_gemm_amd.build        (or fp4_grouped_gemm_amd.build.build())
 
@@ -10,6 +11,7 @@ repository root, the shared libraries next to this file.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
@@ -43,24 +45,27 @@ def _run(cmd: list[str], what: str) -> None:
         raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
 
 
-def build_binding() -> str:
-    """Compile _attention.so against the installed torch and link it to libfgg.so."""
+def _binding(lib: str) -> str | None:
+    """Compile the binding against the installed torch and link it to `lib`
+    (its host side only: there is no kernel in it); returns the built file, not yet in
+    its place.  None if there is no torch: the C ABI does not need one."""
+    if importlib.util.find_spec("torch") is None:
+        return None
     import torch
     home = os.path.dirname(torch.__file__)
     tmp = BINDING + ".tmp"
-    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+    _run([HIPCC, "-x", "hip", "--offload-host-only", "-no-hip-rt", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+          "-DUSE_ROCM",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
           "-I" + os.path.join(ROOT, "include"),
           *(flag for d in (os.path.join(home, "include"),
                            os.path.join(home, "include", "torch", "csrc", "api", "include"),
-                           sysconfig.get_path("include"),
-                           os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"))
+                           sysconfig.get_path("include"))
             for flag in ("-isystem", d)),
-          os.path.join(CSRC, "attention_binding.cpp"), "-o", tmp,
+          os.path.join(CSRC, "attention_binding.cpp"), "-x", "none", lib, "-o", tmp,
           "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_hip", "-lc10",
-          LIB, "-Wl,-rpath,$ORIGIN"], "attention_binding.cpp")
-    os.replace(tmp, BINDING)
-    return BINDING
+          "-Wl,-rpath,$ORIGIN"], "attention_binding.cpp")
+    return tmp
 
 
 def _compile(src: str) -> str:
@@ -99,11 +104,17 @@ def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-Wl,-soname,libfgg.so", *objs, "-o", tmp]
     _run(cmd, "link")
+    # both are built before either is put in its place: a library never stands
+    # beside a binding that was linked to another one
+    binding = _binding(tmp)
+    if binding:
+        os.replace(binding, BINDING)
+    elif os.path.exists(BINDING):
+        os.remove(BINDING)
     os.replace(tmp, LIB)
-    build_binding()
     if verbose:
         print("built", LIB)
-        print("built", BINDING)
+        print("built", BINDING) if binding else print("no torch: the attention binding is not built")
     return LIB
 
 
