@@ -1,5 +1,5 @@
 // Attention operators: the launchers' arguments and the device helpers that
-// the three kernels share (the paged cache, MFMA fragments, wave
+// the three kernels share (the paged cache, types, LDS reads, wave
 // reductions).
 #pragma once
 
@@ -128,33 +128,6 @@ __device__ __forceinline__ u32x2 lds_read_tr(const uint8_t* p) {
 
 __device__ __forceinline__ float xor_max(float v, int off) { return fmaxf(v, __shfl_xor(v, off, 64)); }
 __device__ __forceinline__ float xor_add(float v, int off) { return v + __shfl_xor(v, off, 64); }
-
-// Position of a work item in per-sequence counts: thread t of THREADS holds
-// the counts of entries [t per, (t + 1) per) and calls this with their sum.
-// Every thread gets the total; `base` is the sum over the threads before it.
-// `lds`: THREADS / 64 ints.  All threads call; has two barriers.
-template <int THREADS>
-__device__ __forceinline__ int block_scan(int sum, int& base, int* lds) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  int v = sum;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int u = __shfl_up(v, off, 64);
-    if (lane >= off) v += u;
-  }
-  if (lane == 63) lds[w] = v;
-  __syncthreads();
-  int before = 0, total = 0;
-#pragma unroll
-  for (int i = 0; i < THREADS / 64; ++i) {
-    const int x = lds[i];
-    before += i < w ? x : 0;
-    total += x;
-  }
-  __syncthreads();
-  base = before + v - sum;
-  return total;
-}
 
 }  // namespace attn
 #endif
