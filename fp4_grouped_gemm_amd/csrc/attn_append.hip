@@ -10,8 +10,9 @@
 // are loads and stores of 16 bytes (8 for codes); nothing is read twice but
 // the table, whose rows the heads of a token share in L1/L2.  Bound by HBM, and
 // for small calls by the launch: 16665 tokens of 32 + 8 + 8 heads of 128, all
-// outputs, 80 us for 452 MB (5.6 TB/s; a copy of 2 GiB reaches 4.9); one token 3
-// us on the GPU, 250 tokens of 64 + 8 + 8 heads 5 us.
+// outputs, 81 us for 452 MB (5.6 TB/s; a copy reaches 5.1), and 80 us for 418 MB with
+// an E4M3 cache, whose exact division of each cached value lies under the memory's
+// time; one token 3 us on the GPU, 250 tokens of 64 + 8 + 8 heads 5 us.
 #include "attn.h"
 
 namespace fgg {

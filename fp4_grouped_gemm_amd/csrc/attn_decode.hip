@@ -12,9 +12,12 @@
 // itself, so nothing is read on the host and rows of any lengths balance.
 // A row that lies in one slice is finished there; the pieces of the others
 // are joined by a second kernel.  Measured: 64 sequences of 12000 to 32768
-// tokens, 16 KV heads of 64, 804 us (5.4 GB, 6.8 TB/s); 128 of 2000 to 8191, 8 KV
-// heads of 128 in E4M3, 198 us (5.9 TB/s); 96 of 1 to 6000 65 us (4.7 TB/s); one
-// of 130001 on 4 KV heads 53 us (5.0 TB/s), 6 of them the join.
+// tokens, 16 KV heads of 64, 804 us (5.4 GB, 6.8 TB/s; a kernel that only reads
+// reaches 7.0), in E4M3 478 us (5.7 TB/s); 128 of 2000 to 8191, 8 KV heads of 128 in
+// E4M3, 198 us (5.9 TB/s); 96 of 1 to 6000 66 us (4.7 TB/s); one of 130001 on 4 KV
+// heads 52 us (5.1 TB/s), 6 of them the join.  Where a KV head has more than 16
+// query heads its cache is read once for each 16 (64 sequences of 12000 to 32768
+// tokens, one KV head of 128: 117 us with 16 query heads, 220 with 32).
 //
 // A wave takes 32 tokens of a tile.  S^T = K Q^T on 16x16x32 MFMAs: the A
 // operand of lane l is row (token) l % 16, loaded from the cache straight
@@ -24,9 +27,11 @@
 // 16 a + 4 (l / 16) + i: P never leaves its lane.  The A operand V^T comes
 // from LDS by transposed reads of 4 tokens each.  The matrix cores take BF16,
 // so a weight goes in as the sum of two BF16 values, 16 bits in all: the
-// second product costs nothing under the memory's time (221.2 against 220.3 us
-// for 128 sequences of 2000 to 8191 tokens in E4M3) and takes the weights'
-// rounding out of the result.  Scores, maxima, sums and outputs are FP32.
+// second product costs next to nothing under the memory's time (197.4 against
+// 196.2 us for 128 sequences of 2000 to 8191 tokens in E4M3, nothing in BF16) and
+// takes the weights' rounding out of the result.  Scores, maxima, sums and
+// outputs are FP32.  (A weight below 2^-110 has a second half of 0: times an
+// infinite value that is NaN, where the first half gives infinity.)
 #include "attn.h"
 #include "attn_list.h"
 
@@ -45,11 +50,11 @@ constexpr int kMaxHeads = 16;  // query heads of a KV head in one row of work
 // three waves a SIMD: three workgroups of four waves that share the list, or
 // one of twelve that takes a whole row.  The latter needs no join and no second
 // launch; its waves take 384 tokens at once.  It is taken for tables of one such
-// step (a call on a row of 300 tokens 7.3 us, and two launches take the host 9.3),
-// of two where the rows fill half of the card (240 rows of 700 tokens 16.9 against
-// 22.2 us, 128 rows 14.9 either way; a row of 517 tokens 9.2 against 9.3, of 700
-// 11.1 against 9.3 us), and of four where they fill it (256 rows of 1000 tokens
-// 26.4 against 33.6 us, 1024 rows 100 against 103 us).
+// step (one sequence of 300 tokens, 8 KV heads: 7.2 against 8.8 us), of two where
+// the rows fill half of the card (240 rows of 700 tokens 18.4 against 23.5 us, 128
+// rows 16.0 against 15.8; one sequence of 517 tokens 9.3 against 8.9, of 700 11.1
+// against 8.9 us), and of four where they fill it (256 rows of 1000 tokens 23.6
+// against 29.0 us, 1024 rows 90.6 against 91.1 us).
 constexpr int kListWaves = attn_list::kWaves, kListPerCu = 3;
 constexpr int kWholeWaves = 12;
 constexpr int kWholeStep = kWholeWaves * kWaveTokens;
@@ -74,7 +79,8 @@ __device__ __host__ __forceinline__ bool joins_by_row(int rows, int workgroups) 
 // A load of what this launch does not read again.  Keys and values of a batch
 // are far more than the caches hold, and a load that does not displace what
 // they hold reads faster: 64 sequences of 12000 to 32768 tokens 804 against 891
-// us (6.8 against 6.1 TB/s), 96 of 1 to 6000 65 against 73 us.
+// us (6.8 against 6.1 TB/s), 128 of 2000 to 8191 in E4M3 198 against 220, 96 of 1 to
+// 6000 66 against 73 us.
 __device__ __forceinline__ u32x4 once(const uint8_t* p) {
   return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
 }

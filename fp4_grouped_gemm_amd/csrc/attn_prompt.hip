@@ -11,18 +11,23 @@
 // O^T = V^T P^T as they stand (contraction slot 8 h + 4 a + i of step s is
 // token 16 s + 8 a + 4 h + i), with V^T read from LDS by transposed reads: the
 // weights never leave their lane, and the two lanes of a query meet only when
-// its maximum moves.  P is rounded to BF16, the matrix cores' input type;
-// scores, maxima, sums and outputs are FP32.
+// its maximum moves.  Scores, maxima, sums and outputs are FP32.  The weights are
+// rounded to BF16, the matrix cores' input type; the sum that they are divided by
+// is that of the rounded ones.  Against FP64 the result is off by 0.0018 to 0.0020
+// of its size, 0.0016 of that the output's own rounding; as sums of two BF16
+// values, which take the products with V twice, they add nothing to it, and 32
+// heads of 128, prompts of 4096 and 8192 tokens, take 842 instead of 626 us, 24
+// prompts of 17 to 1501 tokens on heads of 64 60 instead of 48.
 //
 // Four waves share the keys and values of a KV head through LDS, which direct
 // loads fill 64 keys ahead.  Heads of 128 are bound by the matrix cores and the
 // power they draw: 4 D operations a query and key.  Measured: 32 heads of 128,
-// prompts of 4096 and 8192 tokens, 617 us, 1113 TFLOP/s, where a matrix product
-// of 16384^3 reaches 1359; MFMAs busy 64% of the cycles, at a clock of 1.75 GHz;
+// prompts of 4096 and 8192 tokens, 620 us, 1108 TFLOP/s, where a matrix product
+// of 16384^3 reaches 1374; MFMAs busy 64% of the cycles, at a clock of 1.75 GHz;
 // the same without loads or without softmax 566 us, without both 490 us.  Heads
 // of 64 are bound by vector instructions: 55 plain ones and 16 exponentials (of
-// four times the cycles) to 8 MFMAs a block; the same prompts 354 us, 970
-// TFLOP/s; 24 prompts of 17 to 1501 tokens 48 us.
+// four times the cycles) to 8 MFMAs a block; the same prompts 356 us, 965
+// TFLOP/s; 24 prompts of 17 to 1501 tokens 49 us.
 //
 // A masked value must not reach the output even where it is infinite or NaN:
 // masked scores are overwritten, but in the product with V a weight of 0
@@ -117,8 +122,8 @@ __device__ __forceinline__ float half_max(float v) {
 }
 
 // Registers and LDS are for two workgroups on a compute unit, with heads of 64
-// for four: a short tile spends more time on its start and end than on its keys
-// (24 prompts of 17 to 1501 tokens 58 with four against 61 us with three).
+// for four: a short tile spends more time on its start and end than on its keys.
+// (Bounds of three and four take the same time.)
 template <int D, int KG, int HP>
 __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void prompt_kernel(PromptArgs a) {
   static_assert(HP == 1 || KG == 1, "waves take several heads or several parts of the keys");
@@ -603,8 +608,8 @@ hipError_t launch(const PromptArgs& a, hipStream_t s) {
 // Heads of one KV head that the waves of a workgroup take, where the keys are not
 // split: as many of four as divide the group.  Fewer queries then make up the
 // rows, and less is computed for nothing on the diagonal (24 prompts of 17 to
-// 1501 tokens, D = 64: 54 against 59 us; nothing gained on 8192 tokens, nor where
-// the keys are split).
+// 1501 tokens, D = 64, three sets of inputs in turn: 52 against 56 us with one head
+// a workgroup; nothing gained on 8192 tokens, nor where the keys are split).
 static int heads_together(int q_heads, int kv_heads) {
   const int group = q_heads / kv_heads;
   return group % 4 == 0 ? 4 : group % 2 == 0 ? 2 : 1;
@@ -620,14 +625,14 @@ hipError_t launch(const PromptArgs& a, hipStream_t s) {
   // that would leave compute units without work or with one (long) item each,
   // halves of them, split over the keys, spread better: up to as many items as
   // compute units, or twice as many of heads of 64, four of which fit on one.
-  // Measured, whole against split: 8 heads of 128, 4001 tokens 60 against 49 us, 32
-  // of 1000 22 against 20 us, but 32 of 2048 46 against 52 us; 32 heads of 64,
-  // 1500 tokens 24.3 against 20.4 us, 2048 33.2 against 31.1 us, 4096 no difference.
+  // Measured, whole against split: 8 heads of 128, 4001 tokens 68 against 52 us, 32
+  // of 1000 22.2 against 19.1 us, but 32 of 2048 46 against 49 us; 32 heads of 64,
+  // 1500 tokens 21.8 against 18.3 us, 2048 30.7 against 28.5 us, 4096 86.9 against 86.1.
   // A split costs each workgroup a join and a larger tile per prompt, so
   // prompts have to be long for it, the longer the fuller the card is already (32
-  // heads of 128, 20 prompts of 30 tokens 7.8 against 12.1 us, 4 of 200 10.3 against
-  // 11.6 us, 2 of 400 13.0 against 12.9 us; 16 heads, 3 of 200 9.6 against 9.0 us; of
-  // 64, 4 of 500 13.1 against 13.7 us).
+  // heads of 128, 20 prompts of 30 tokens 7.1 against 11.7 us, 4 of 200 10.1 against
+  // 11.2 us, 2 of 400 12.8 against 12.4 us; 16 heads, 3 of 200 9.1 against 8.2 us; of
+  // 64, 4 of 500 13.7 either way).
   const long long items = (long long)((a.T + 127) / 128) * a.q_heads;
   const bool split = items <= (D == 64 ? 2 : 1) * a.num_cus && items * 448 * a.batch <= (long long)a.num_cus * a.T;
   if (split) return launch<D, 2, 1>(a, s);

@@ -448,7 +448,8 @@ void fgg_tune_clear(void);
  * not attended to.  k_strides and v_strides are in values between pages,
  * heads and tokens, in any order of these three (head_dim is contiguous):
  * both [pages, heads, tokens, dim] and [pages, tokens, heads, dim] pools
- * are described as they are, and K and V may share a pool.
+ * are described as they are, and K and V may share a pool.  kv_heads <= 2^10,
+ * q_heads <= 2^12 and a multiple of kv_heads, batch <= 2^20.
  * ------------------------------------------------------------------------ */
 #define FGG_KV_BF16 0
 #define FGG_KV_E4M3 1
@@ -493,6 +494,7 @@ typedef struct {
  * E4M3FN(clamp(x / scale, +-448)) (NaN stays NaN).  Scales must be positive.
  * Two tokens with the same place leave either's values there.
  * rot_dim: a multiple of 16 (an even one that is not: FGG_EUNSUPPORTED).
+ * T <= 2^24 and T * (q_heads + 2 kv_heads) * head_dim / 16 < 2^31.
  */
 fgg_status rope_kv_append(const fgg_kv_cache* cache, const void* q, const void* k, const void* v,
                           const long long* strides, const float* turns, int num_turns, int rot_dim,
@@ -517,9 +519,12 @@ fgg_status rope_kv_append(const fgg_kv_cache* cache, const void* q, const void* 
  *            contents need no initialisation and are free after the call's
  *            work on `stream` is done.
  *
+ * batch * q_heads * (table_width * page_size / 128 + 1) <= 2^30, and a table
+ * below 2^31 tokens (else FGG_EUNSUPPORTED).
+ *
  * Scores, maxima, sums and outputs are FP32; the weights p_t enter the
- * product with V to 16 bits, as sums of two BF16 values.  What the cache holds past a sequence's
- * length never reaches an output, NaN included.
+ * product with V to 16 bits, as sums of two BF16 values.  What the cache
+ * holds past a sequence's length never reaches an output, NaN included.
  */
 fgg_status paged_decode_attention_workspace(const fgg_kv_cache* cache, int q_heads, size_t* bytes);
 fgg_status paged_decode_attention(const fgg_kv_cache* cache, const void* q, long long q_seq_stride,
