@@ -17,11 +17,15 @@ import ctypes
 import os
 
 from .attention import paged_decode_attention, prompt_attention, rope_kv_append
+from .mxfp4 import (dequantize_mxfp4, grouped_mxfp4_gated_gemm, grouped_mxfp4_gemm, mxfp4_gated_gemm,
+                    mxfp4_gemm, quantize_mxfp4, residual_norm)
 
 __all__ = [
     "grouped_fp8_gemm", "fp4_gemm", "grouped_fp4_gemm", "quantize_fp8_1x128",
     "quantize_nvfp4", "grouped_fp8_gemm_tune", "fp4_gemm_tune", "grouped_fp4_gemm_tune",
     "tuned_tile", "tune_clear", "fp4_gemm_problems", "fp8_gemm_problems", "grouped_w4a16_gemm",
+    "quantize_mxfp4", "dequantize_mxfp4", "mxfp4_gemm", "grouped_mxfp4_gemm", "mxfp4_gated_gemm",
+    "grouped_mxfp4_gated_gemm", "residual_norm",
     "rank_tiles", "rope_kv_append", "paged_decode_attention", "prompt_attention",
     "num_tiles",
     "device_info", "library_path", "load_library", "FP8", "FP4",
@@ -112,6 +116,14 @@ def load_library():
         ("fp4_gemm_tune", [P, P, P, P, F, P, I, I, I, I, I, REP, OPT, P]),
         ("grouped_fp4_gemm_tune", [P, P, P, P, P, F, P, I, I, I, I, I, I, REP, OPT, P]),
         ("fgg_tuned_tile", [I, I, I, I, I]),
+        ("quantize_mxfp4", [P, P, P, I, I, P]),
+        ("quantize_mxfp4_rows", [P, P, P, P, I, I, I, P]),
+        ("dequantize_mxfp4", [P, P, P, I, I, P]),
+        ("mxfp4_gemm", [P, P, P, P, P, I, I, I, P]),
+        ("grouped_mxfp4_gemm", [P, P, P, P, P, P, I, I, I, I, P]),
+        ("mxfp4_gated_gemm", [P, P, P, P, P, P, I, I, I, P]),
+        ("grouped_mxfp4_gated_gemm", [P, P, P, P, P, P, P, I, I, I, I, P]),
+        ("residual_norm", [P, P, P, ctypes.POINTER(ctypes.c_longlong), P, P, F, F, P, P, P, I, I, P]),
     ):
         fn = getattr(lib, name)
         fn.restype = ctypes.c_int

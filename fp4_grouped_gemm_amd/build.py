@@ -25,7 +25,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfgg.so")
 
 SOURCES = ["api.cpp", "fp8_grouped.hip", "fp4.hip", "quant.hip", "w4a16.hip",
-           "attn_append.hip", "attn_decode.hip", "attn_prompt.hip"]
+           "attn_append.hip", "attn_decode.hip", "attn_prompt.hip", "mx_rows.hip", "norm.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
@@ -62,7 +62,7 @@ def _binding(lib: str) -> str | None:
                            os.path.join(home, "include", "torch", "csrc", "api", "include"),
                            sysconfig.get_path("include"))
             for flag in ("-isystem", d)),
-          os.path.join(CSRC, "attention_binding.cpp"), "-x", "none", lib, "-o", tmp,
+          os.path.join(CSRC, "attention_binding.cpp"), os.path.join(CSRC, "mxfp4_binding.cpp"), "-x", "none", lib, "-o", tmp,
           "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_hip", "-lc10",
           "-Wl,-rpath,$ORIGIN"], "attention_binding.cpp")
     return tmp

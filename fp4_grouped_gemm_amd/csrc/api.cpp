@@ -25,6 +25,7 @@
 #include "../../include/fgg.h"
 #include "attn.h"
 #include "common.h"
+#include "mx.h"
 
 namespace {
 
@@ -742,6 +743,138 @@ fgg_status quantize_nvfp4_static_rows(const void* X, const int32_t* rows, void* 
                                                      static_cast<uint8_t*>(scale), global_scale, R,
                                                      K, d->num_cus,
                                                      static_cast<hipStream_t>(stream), rows, T));
+}
+
+// -------------------------------------------------------------------- MXFP4
+fgg_status quantize_mxfp4(const void* X, void* Q, void* scale, int M, int K, void* stream) {
+  const char* fn = "quantize_mxfp4";
+  fgg_status st = check_quant(fn, X, Q, scale, M, K, 1, 32);
+  if (st != FGG_OK) return st;
+  const DeviceFacts* d = current_device(fn, &st);
+  if (!d) return st;
+  return launched(fn, fgg::launch_quant_mxfp4(static_cast<const uint16_t*>(X), static_cast<uint8_t*>(Q),
+                                              static_cast<uint8_t*>(scale), M, K, d->num_cus,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+fgg_status quantize_mxfp4_rows(const void* X, const int32_t* rows, void* Q, void* scale, int R, int T,
+                               int K, void* stream) {
+  const char* fn = "quantize_mxfp4_rows";
+  fgg_status st = check_quant(fn, X, Q, scale, R, K, 1, 32);
+  if (st != FGG_OK) return st;
+  if ((st = check_rows(fn, rows, R, T, K)) != FGG_OK) return st;
+  const DeviceFacts* d = current_device(fn, &st);
+  if (!d) return st;
+  return launched(fn, fgg::launch_quant_mxfp4(static_cast<const uint16_t*>(X), static_cast<uint8_t*>(Q),
+                                              static_cast<uint8_t*>(scale), R, K, d->num_cus,
+                                              static_cast<hipStream_t>(stream), rows, T));
+}
+
+fgg_status dequantize_mxfp4(const void* Q, const void* scale, void* X, int M, int K, void* stream) {
+  const char* fn = "dequantize_mxfp4";
+  fgg_status st = check_quant(fn, X, Q, scale, M, K, 1, 32);
+  if (st != FGG_OK) return st;
+  const DeviceFacts* d = current_device(fn, &st);
+  if (!d) return st;
+  return launched(fn, fgg::launch_dequant_mxfp4(static_cast<const uint8_t*>(Q),
+                                                static_cast<const uint8_t*>(scale),
+                                                static_cast<uint16_t*>(X), M, K, d->num_cus,
+                                                static_cast<hipStream_t>(stream)));
+}
+
+// Every MXFP4 product: dense ones have no m_indices and G = 1.
+static fgg_status mx_gemm(const char* fn, const void* A, const void* B, const void* a_scale,
+                          const void* b_scale, const int32_t* m_indices, void* C, void* c_scale, int M,
+                          int N, int K, int G, bool grouped, bool gated, void* stream) {
+  const char* const n = gated ? "F" : "N";
+  if (!A || !B || !a_scale || !b_scale || !C)
+    return fail(FGG_EINVAL, fn, "null pointer among A, B, a_scale, b_scale, C");
+  if (grouped && !m_indices) return fail(FGG_EINVAL, fn, "m_indices is null");
+  if (M < 1 || M > (1 << 24)) return fail(FGG_EINVAL, fn, "requires 1 <= M <= 2^24, got M=%d", M);
+  if (N < 16 || N > (1 << 19)) return fail(FGG_EINVAL, fn, "requires 16 <= %s <= 2^19, got %s=%d", n, n, N);
+  if (K < 32 || K > (1 << 20)) return fail(FGG_EINVAL, fn, "requires 32 <= K <= 2^20, got K=%d", K);
+  if (K % 32) return fail(FGG_EINVAL, fn, "requires K %% 32 == 0, got K=%d", K);
+  if (c_scale && N % 32) return fail(FGG_EINVAL, fn, "an MXFP4 result requires F %% 32 == 0, got F=%d", N);
+  if (G < 1 || G > (1 << 16)) return fail(FGG_EINVAL, fn, "requires 1 <= G <= 2^16, got G=%d", G);
+  if (N % 16) return fail(FGG_EUNSUPPORTED, fn, "%s %% 16 != 0 (%s=%d) is not supported", n, n, N);
+  if (K % 128)
+    return fail(FGG_EUNSUPPORTED, fn, "K %% 128 != 0 (K=%d) is not supported: whole 128-wide K steps only", K);
+  if ((long long)((N + 15) / 16) * G >= 1 << 23)  // a launch takes fewer than 2^32 threads
+    return fail(FGG_EUNSUPPORTED, fn, "requires ceil(%s / 16) * G < 2^23, got %s=%d G=%d", n, n, N, G);
+  if (!aligned(A, 16) || !aligned(B, 16) || !aligned(C, 16))
+    return fail(FGG_EALIGN, fn, "A, B and C must be 16-byte aligned");
+  if (!aligned(a_scale, 4) || !aligned(b_scale, 4))
+    return fail(FGG_EALIGN, fn, "a_scale and b_scale must be 4-byte aligned");
+  if (!aligned(m_indices, 4)) return fail(FGG_EALIGN, fn, "m_indices must be 4-byte aligned");
+  fgg_status st;
+  const DeviceFacts* d = current_device(fn, &st);
+  if (!d) return st;
+  const fgg::MxGemmArgs a{static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(B),
+                          static_cast<const uint8_t*>(a_scale), static_cast<const uint8_t*>(b_scale),
+                          grouped ? m_indices : nullptr, static_cast<uint8_t*>(C),
+                          static_cast<uint8_t*>(c_scale), M, N, K, G, gated, d->num_cus};
+  return launched(fn, fgg::launch_mx_gemm(a, static_cast<hipStream_t>(stream)));
+}
+
+fgg_status mxfp4_gemm(const void* A, const void* B, const void* a_scale, const void* b_scale, void* C,
+                      int M, int N, int K, void* stream) {
+  return mx_gemm("mxfp4_gemm", A, B, a_scale, b_scale, nullptr, C, nullptr, M, N, K, 1, false, false, stream);
+}
+
+fgg_status grouped_mxfp4_gemm(const void* A, const void* B, const void* a_scale, const void* b_scale,
+                              const int32_t* m_indices, void* C, int M, int N, int K, int G, void* stream) {
+  return mx_gemm("grouped_mxfp4_gemm", A, B, a_scale, b_scale, m_indices, C, nullptr, M, N, K, G, true, false,
+                 stream);
+}
+
+fgg_status mxfp4_gated_gemm(const void* A, const void* B, const void* a_scale, const void* b_scale, void* C,
+                            void* c_scale, int M, int F, int K, void* stream) {
+  return mx_gemm("mxfp4_gated_gemm", A, B, a_scale, b_scale, nullptr, C, c_scale, M, F, K, 1, false, true,
+                 stream);
+}
+
+fgg_status grouped_mxfp4_gated_gemm(const void* A, const void* B, const void* a_scale, const void* b_scale,
+                                    const int32_t* m_indices, void* C, void* c_scale, int M, int F, int K,
+                                    int G, void* stream) {
+  return mx_gemm("grouped_mxfp4_gated_gemm", A, B, a_scale, b_scale, m_indices, C, c_scale, M, F, K, G, true,
+                 true, stream);
+}
+
+// Rows of BF16 values read in 16-byte pieces.
+static fgg_status check_vectors(const char* fn, const char* name, const void* p, long long row) {
+  if (row < 0) return fail(FGG_EINVAL, fn, "%s has a negative stride", name);
+  if (!aligned(p, 16) || row % 8)
+    return fail(FGG_EALIGN, fn, "%s must be 16-byte aligned, its row stride a multiple of 8 values", name);
+  return FGG_OK;
+}
+
+fgg_status residual_norm(const void* x, const void* residual, const void* gate, const long long* strides,
+                         const void* post_weight, const void* weight, float scale, float eps, void* h, void* y,
+                         void* y_scale, int T, int H, void* stream) {
+  const char* fn = "residual_norm";
+  if (!x || !strides || !weight || !h || !y)
+    return fail(FGG_EINVAL, fn, "null pointer among x, strides, weight, h, y");
+  if (T < 1 || T >= (1 << 24)) return fail(FGG_EINVAL, fn, "requires 1 <= T < 2^24, got T=%d", T);
+  if (H < 1 || H > (1 << 20)) return fail(FGG_EINVAL, fn, "requires 1 <= H <= 2^20, got H=%d", H);
+  if (y_scale && H % 32) return fail(FGG_EINVAL, fn, "an MXFP4 result requires H %% 32 == 0, got H=%d", H);
+  if (H % (y_scale ? 128 : 8))
+    return fail(FGG_EUNSUPPORTED, fn, "H %% %d != 0 (H=%d) is not supported", y_scale ? 128 : 8, H);
+  if (!std::isfinite(scale)) return fail(FGG_EINVAL, fn, "scale must be finite");
+  if (!std::isfinite(eps) || eps < 0) return fail(FGG_EINVAL, fn, "eps must be finite and not negative");
+  fgg_status st;
+  if ((st = check_vectors(fn, "x", x, strides[0])) != FGG_OK) return st;
+  if ((st = check_vectors(fn, "residual", residual, residual ? strides[1] : 0)) != FGG_OK) return st;
+  if ((st = check_vectors(fn, "gate", gate, gate ? strides[2] : 0)) != FGG_OK) return st;
+  if (!aligned(post_weight, 16) || !aligned(weight, 16) || !aligned(h, 16) || !aligned(y, 16))
+    return fail(FGG_EALIGN, fn, "post_weight, weight, h and y must be 16-byte aligned");
+  const DeviceFacts* d = current_device(fn, &st);
+  if (!d) return st;
+  const fgg::NormArgs a{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(residual),
+                        static_cast<const uint16_t*>(gate), static_cast<const uint16_t*>(post_weight),
+                        static_cast<const uint16_t*>(weight), strides[0], strides[1], strides[2],
+                        static_cast<uint16_t*>(h), static_cast<uint8_t*>(y), static_cast<uint8_t*>(y_scale),
+                        scale, eps, T, H};
+  return launched(fn, fgg::launch_norm(a, static_cast<hipStream_t>(stream)));
 }
 
 // ---------------------------------------------------------------- attention

@@ -6,62 +6,20 @@
 // The functions take attention.py's arguments by position, run on the current
 // stream of their operands' device, and raise ValueError for everything that they
 // or the library refuse.
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
-#include <torch/csrc/utils/object_ptr.h>
-
-#include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
-#include <c10/core/DeviceGuard.h>
-#include <c10/hip/HIPStream.h>
-
 #include <array>
 #include <cmath>
-#include <cstdint>
 
-#include "fgg.h"
+#include "binding.h"
 
 namespace {
 
-using at::Tensor;
-
-const char* type_name(at::ScalarType t) {
-  return t == at::kBFloat16 ? "torch.bfloat16" : t == at::kInt ? "torch.int32" : t == at::kFloat ? "torch.float32"
-                                                                                                : c10::toString(t);
-}
-
-const Tensor& tensor(PyObject* o, const char* name, at::ScalarType dtype, int64_t dim) {
-  const bool is = THPVariable_Check(o) && THPVariable_Unpack(o).scalar_type() == dtype &&
-                  THPVariable_Unpack(o).dim() == dim;
-  TORCH_CHECK_VALUE(is, name, " must be a ", dim, "-D ", type_name(dtype), " tensor");
-  const Tensor& t = THPVariable_Unpack(o);
-  TORCH_CHECK_VALUE(t.is_cuda(), name, " must be a GPU tensor");
-  return t;
-}
-
-void on(const Tensor& t, const char* name, const Tensor& q) {
-  TORCH_CHECK_VALUE(t.get_device() == q.get_device(), name, " is on ", t.device(), ", expected ", q.device());
-}
+using namespace fgg_binding;
 
 // A BF16 [rows, heads, head_dim] operand, head_dim contiguous.
 const Tensor& heads(PyObject* o, const char* name) {
   const Tensor& t = tensor(o, name, at::kBFloat16, 3);
   TORCH_CHECK_VALUE(t.stride(2) == 1, name, " must be contiguous in its last dimension");
   return t;
-}
-
-// Stride of a dimension; one that holds a single entry may have any.
-long long step(const Tensor& t, int dim) { return t.size(dim) > 1 ? t.stride(dim) : 0; }
-
-// A contiguous vector of n values on q's device; any length if n is negative.
-template <class T>
-const T* vector(PyObject* o, const char* name, int64_t n, at::ScalarType dtype, const Tensor& q) {
-  const Tensor& t = tensor(o, name, dtype, 1);
-  on(t, name, q);
-  TORCH_CHECK_VALUE(t.is_contiguous() && (n < 0 || t.size(0) == n), name, " must be a contiguous ",
-                    type_name(dtype), " tensor", n < 0 ? "" : " of shape (", n < 0 ? "" : std::to_string(n),
-                    n < 0 ? "" : ",)");
-  return static_cast<const T*>(t.const_data_ptr());
 }
 
 // A 2-D tensor on q's device, its last dimension contiguous.
@@ -129,40 +87,11 @@ Tensor result(PyObject* out, const Tensor& q, int64_t rows, int64_t n, int64_t d
   return t;
 }
 
-// Runs a call of the library without the interpreter's lock (a launch can wait for
-// room in the stream's queue).
-template <class F>
-void call(F f) {
-  PyThreadState* const state = PyEval_SaveThread();
-  const fgg_status st = f();
-  PyEval_RestoreThread(state);
-  if (st == FGG_OK) return;
-  const char* msg = fgg_last_error();
-  TORCH_CHECK_VALUE(false, msg && *msg ? msg : "fgg call failed");
-}
-
-int as_int(int64_t n, const char* name) {
-  TORCH_CHECK_VALUE(n <= INT32_MAX, name, " passes 2^31");
-  return (int)n;
-}
-
 float scale_of(PyObject* o, int64_t dim) {
   if (o == Py_None) return 1.0f / std::sqrt((float)dim);
   const double x = PyFloat_AsDouble(o);
   if (x == -1.0 && PyErr_Occurred()) throw python_error();
   return (float)x;
-}
-
-bool truth(PyObject* o) {
-  const int x = PyObject_IsTrue(o);
-  if (x < 0) throw python_error();
-  return x;
-}
-
-void* stream_on(const Tensor& q) { return c10::hip::getCurrentHIPStream(q.get_device()).stream(); }
-
-void arity(Py_ssize_t n, Py_ssize_t want) {
-  TORCH_CHECK_VALUE(n == want, "expected ", want, " arguments, got ", n);
 }
 
 // q, k, v, cos_sin, positions, page_table, k_cache, v_cache, seq_ids, interleaved,
@@ -265,13 +194,10 @@ PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
-PyMethodDef method(const char* name) {
-  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(F)), METH_FASTCALL, nullptr};
-}
-
 PyMethodDef methods[] = {method<append>("rope_kv_append"), method<decode>("paged_decode_attention"),
-                         method<prompt>("prompt_attention"), {nullptr, nullptr, 0, nullptr}};
+                         method<prompt>("prompt_attention"), method<quantize>("quantize_mxfp4"),
+                         method<dequantize>("dequantize_mxfp4"), method<product>("mxfp4_product"),
+                         method<norm>("residual_norm"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attention", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,6 +1,8 @@
 // Activation quantisers for gfx950: BF16 -> FP8 E4M3FN with one FP32 scale
-// per row and 128-wide K block, and BF16 -> NVFP4 (E2M1 codes, one E4M3
-// scale per 16 elements, one FP32 global scale).  The step before the GEMM.
+// per row and 128-wide K block, BF16 -> NVFP4 (E2M1 codes, one E4M3
+// scale per 16 elements, one FP32 global scale), and BF16 -> MXFP4 (E2M1
+// codes, one power of two per 32 elements; mx.h) and back.  The step before
+// the GEMM.
 //
 // What is computed (sglang#27745 page, "Code analysis 1: FP8 quantisation":
 // clamp to +-448, the gfx950 E4M3FN maximum, then encode; the per-128 FP32
@@ -17,11 +19,12 @@
 // input alone.  Codes come from the hardware pack converts (round to
 // nearest even; the inputs are clamped first, so saturation never applies).
 //
-// Both kernels treat X as a flat array of M * K values: K is a multiple of
+// The kernels treat X as a flat array of M * K values: K is a multiple of
 // 128, so no block crosses a row, and the scale arrays are the blocks in
-// flat order.  They are HBM-bound: 2 bytes read and 1 (FP8) or 0.5 (NVFP4)
+// flat order.  They are HBM-bound: 2 bytes read and 1 (FP8) or 0.5 (FP4)
 // written per value.
 #include "common.h"
+#include "mx.h"
 
 #include <climits>
 
@@ -311,6 +314,52 @@ __global__ void finalize_kernel(uint32_t* g) {
   g[0] = __float_as_uint(global_scale(g[0]));
 }
 
+// ------------------------------------------------------------------ MXFP4
+// A lane holds a whole 32-value block.
+__global__ __launch_bounds__(kQThreads) void quant_mxfp4_kernel(const uint16_t* __restrict__ X,
+                                                                uint8_t* __restrict__ Q,
+                                                                uint8_t* __restrict__ S,
+                                                                long long nblocks, RowMap map) {
+  const long long stride = (long long)gridDim.x * kQThreads;
+  for (long long q = (long long)blockIdx.x * kQThreads + threadIdx.x; q < nblocks; q += stride) {
+    float v[4][8];
+    load_piece(X, q, map, v);
+    uint32_t top = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) top = max(top, mx::top8(v[u]));
+    const uint32_t code = mx::scale_code(top);
+    const float inv = mx::inverse(code);
+    u32x4 codes = {0u, 0u, 0u, 0u};
+    if (code != 255u) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) codes[u] = mx::codes8(v[u], inv);
+    }
+    *reinterpret_cast<u32x4*>(Q + q * 16) = codes;
+    S[q] = (uint8_t)code;
+  }
+}
+
+// The values back as BF16: exact where the format reaches them (6 * 2^127
+// rounds to infinity).  A lane takes eight values, so that loads and stores
+// are contiguous over a wave.
+__global__ __launch_bounds__(kQThreads) void dequant_mxfp4_kernel(const uint8_t* __restrict__ Q,
+                                                                  const uint8_t* __restrict__ S,
+                                                                  uint16_t* __restrict__ X,
+                                                                  long long pieces) {
+  const long long stride = (long long)gridDim.x * kQThreads;
+  for (long long i = (long long)blockIdx.x * kQThreads + threadIdx.x; i < pieces; i += stride) {
+    const uint32_t word = reinterpret_cast<const uint32_t*>(Q)[i];
+    const float s = mx::value(S[i >> 2]);
+    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.0f, 0);
+    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.0f, 1);
+    const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.0f, 2);
+    const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, 1.0f, 3);
+    const uint2 lo = pack_bf16x4(a[0] * s, a[1] * s, b[0] * s, b[1] * s);
+    const uint2 hi = pack_bf16x4(c[0] * s, c[1] * s, d[0] * s, d[1] * s);
+    reinterpret_cast<uint4*>(X)[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  }
+}
+
 // Workgroups for `waves` waves of work, at most per_cu per compute unit
 // (the rest loop); measured best: 8 per CU for the streaming loops here.
 int grid_for(long long waves, int num_cus, int per_cu) {
@@ -362,6 +411,26 @@ hipError_t launch_quant_nvfp4_static(const uint16_t* X, uint8_t* Q, uint8_t* S, 
   const RowMap map{rows, (uint32_t)(K / 32), T};
   hipLaunchKernelGGL(quant_nvfp4_kernel, dim3(grid_for((nblocks / 2 + 63) / 64, num_cus, 16)),
                      dim3(kQThreads), 0, s, X, Q, S, (const uint32_t*)nullptr, g, nblocks, map);
+  return hipGetLastError();
+}
+
+hipError_t launch_quant_mxfp4(const uint16_t* X, uint8_t* Q, uint8_t* S, int M, int K, int num_cus,
+                              hipStream_t s, const int32_t* rows, int T) {
+  const long long nblocks = (long long)M * (K / 32);
+  if (nblocks <= 0) return hipSuccess;
+  if (rows && nblocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+  const RowMap map{rows, (uint32_t)(K / 32), T};
+  hipLaunchKernelGGL(quant_mxfp4_kernel, dim3(grid_for((nblocks + 63) / 64, num_cus, 16)),
+                     dim3(kQThreads), 0, s, X, Q, S, nblocks, map);
+  return hipGetLastError();
+}
+
+hipError_t launch_dequant_mxfp4(const uint8_t* Q, const uint8_t* S, uint16_t* X, int M, int K,
+                                int num_cus, hipStream_t s) {
+  const long long pieces = (long long)M * (K / 8);
+  if (pieces <= 0) return hipSuccess;
+  hipLaunchKernelGGL(dequant_mxfp4_kernel, dim3(grid_for((pieces + 63) / 64, num_cus, 16)),
+                     dim3(kQThreads), 0, s, Q, S, X, pieces);
   return hipGetLastError();
 }
 

@@ -437,6 +437,104 @@ int fgg_tuned_tile(int kind, int M, int N, int K, int G);
 void fgg_tune_clear(void);
 
 /* ------------------------------------------------------------------------
+ * MXFP4: E2M1 codes and, for each 32 of them along a row, one power of two --
+ * the 4-bit format whose scales gfx950's matrix instructions take with their
+ * operands.  A row of K values is K / 2 bytes of codes (element 2j in the low
+ * nibble of byte j) and K / 32 E8M0 codes: code e stands for 2^(e - 127), 255
+ * for NaN.
+ *
+ * quantize_mxfp4 -- BF16 X [M, K] -> codes Q [M, K/2], scale [M, K/32].  A
+ * block whose largest magnitude lies in [2^p, 2^(p + 1)) gets the scale
+ * 2^max(p - 2, -127) (a block of zeros 2^-127); its codes are
+ * E2M1(x / scale), rounded to nearest, ties to even, saturating at 6.  A block
+ * with an infinity or a NaN in it gets scale code 255 and codes of zero.
+ *
+ * quantize_mxfp4_rows -- the row expansion of an MoE layer fused in: output
+ * row r quantises X[rows[r]] of X's T rows; an entry outside [0, T) gives a
+ * row of zeros.
+ *
+ * dequantize_mxfp4 -- the values back: X [M, K] = BF16(code * scale), exact but
+ * for 4 * 2^127 and 6 * 2^127, which are infinities.
+ *
+ * Requirements: 1 <= M (R) <= 2^24, 32 <= K <= 2^20 with K % 32 == 0 (else
+ * FGG_EINVAL), K % 128 == 0 (else FGG_EUNSUPPORTED); with rows 1 <= T <= 2^24
+ * and R * K / 32 < 2^31; X and Q 16-byte, rows 4-byte aligned.
+ * ------------------------------------------------------------------------ */
+fgg_status quantize_mxfp4(const void* X, void* Q, void* scale, int M, int K, void* stream);
+fgg_status quantize_mxfp4_rows(const void* X, const int32_t* rows, void* Q, void* scale, int R, int T,
+                               int K, void* stream);
+fgg_status dequantize_mxfp4(const void* Q, const void* scale, void* X, int M, int K, void* stream);
+
+/*
+ * mxfp4_gemm, grouped_mxfp4_gemm -- dense and grouped MXFP4 products, BF16
+ * out:  C[i, n] = sum_k A[i, k] * B[g, n, k],  g = m_indices[i] (dense: 0).
+ *
+ *   A [M, K/2], a_scale [M, K/32];  B [G, N, K/2], b_scale [G, N, K/32]
+ *   m_indices [M]  int32 expert id; any value outside [0, G) is padding, whose
+ *                  rows of C are zeros.  In any order.
+ *   C [M, N]       BF16, written in full
+ *
+ * mxfp4_gated_gemm, grouped_mxfp4_gated_gemm -- the first half of a gated
+ * feed-forward block, both projections, the activation and the product:
+ *   C[i, n] = silu(gate) * up,  silu(x) = x / (1 + exp(-x)),
+ *   gate = sum_k A[i, k] * B[g, n, k],  up = sum_k A[i, k] * B[g, F + n, k]
+ *
+ *   B [G, 2 F, K/2], b_scale [G, 2 F, K/32]: each expert's F gate rows, then
+ *                  its F up rows
+ *   c_scale        NULL: C [M, F] is BF16.  Else C [M, F/2] and c_scale
+ *                  [M, F/32] are the FP32 results in MXFP4 (as
+ *                  quantize_mxfp4 encodes), which the second product takes as
+ *                  its A; rows of padding get codes and scale codes of zero.
+ *
+ * Sums are FP32, rounded once to the result.  A scale code of 255 makes every
+ * result that it reaches NaN.  Rows of padding may hold any bytes.
+ *
+ * Requirements: 1 <= M <= 2^24, 16 <= N (F) <= 2^19, 32 <= K <= 2^20 with
+ * K % 32 == 0, 1 <= G <= 2^16, F % 32 == 0 for an MXFP4 result (else
+ * FGG_EINVAL); N (F) % 16 == 0, K % 128 == 0 and ceil(N / 16) * G < 2^23 (else
+ * FGG_EUNSUPPORTED); A, B and C 16-byte, a_scale, b_scale and m_indices 4-byte
+ * aligned (else FGG_EALIGN).
+ */
+fgg_status mxfp4_gemm(const void* A, const void* B, const void* a_scale, const void* b_scale, void* C,
+                      int M, int N, int K, void* stream);
+fgg_status grouped_mxfp4_gemm(const void* A, const void* B, const void* a_scale, const void* b_scale,
+                              const int32_t* m_indices, void* C, int M, int N, int K, int G,
+                              void* stream);
+fgg_status mxfp4_gated_gemm(const void* A, const void* B, const void* a_scale, const void* b_scale,
+                            void* C, void* c_scale, int M, int F, int K, void* stream);
+fgg_status grouped_mxfp4_gated_gemm(const void* A, const void* B, const void* a_scale,
+                                    const void* b_scale, const int32_t* m_indices, void* C,
+                                    void* c_scale, int M, int F, int K, int G, void* stream);
+
+/*
+ * residual_norm -- the border between two blocks: a block's output, normed
+ * and gated, is added to the residual, and the sum is normed for the next.
+ *
+ *   u = x, or with post_weight  post_weight * x / sqrt(mean(x^2) + eps)
+ *   h = residual + scale * gate * u
+ *   y = weight * h / sqrt(mean(h^2) + eps)
+ *
+ *   x, residual, gate  BF16 [T, H], rows strides = {x, residual, gate} values
+ *                      apart (multiples of 8; 0 repeats one row, as a gate
+ *                      per channel does); residual NULL: 0, gate NULL: 1
+ *   post_weight, weight  BF16 [H]; post_weight NULL: x is not normed
+ *   h                  BF16 [T, H], written; must not overlap x, residual or
+ *                      gate
+ *   y                  BF16 [T, H] if y_scale is NULL, else MXFP4 codes
+ *                      [T, H/2] with y_scale [T, H/32], encoded as by
+ *                      quantize_mxfp4 from the FP32 results
+ *
+ * FP32 throughout; y is computed from h before h is rounded.  Squares past
+ * FP32's range are infinite.  1 <= T < 2^24, 1 <= H <= 2^20, eps >= 0; H % 8
+ * == 0, H % 128 == 0 for an MXFP4 result (else FGG_EUNSUPPORTED, or FGG_EINVAL
+ * where that needs whole blocks of 32).
+ */
+fgg_status residual_norm(const void* x, const void* residual, const void* gate,
+                         const long long* strides, const void* post_weight, const void* weight,
+                         float scale, float eps, void* h, void* y, void* y_scale, int T, int H,
+                         void* stream);
+
+/* ------------------------------------------------------------------------
  * Attention of the layers around the experts: the append of new keys and
  * values to a paged cache, one new token a sequence against that cache, and
  * whole prompts.
