@@ -25,7 +25,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfgg.so")
 
 SOURCES = ["api.cpp", "fp8_grouped.hip", "fp4.hip", "quant.hip", "w4a16.hip",
-           "attn_append.hip", "attn_decode.hip", "attn_prompt.hip", "mx_rows.hip", "norm.hip"]
+           "attn_append.hip", "attn_decode.hip", "attn_prompt.hip", "mx_rows.hip", "mx_tiles.hip",
+           "norm.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

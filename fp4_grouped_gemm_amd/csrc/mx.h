@@ -43,6 +43,8 @@ struct NormArgs {
 };
 
 hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t s);
+hipError_t launch_mx_rows(const MxGemmArgs& a, hipStream_t s);                // few rows: a stream of the weights
+hipError_t launch_mx_tiles(const MxGemmArgs& a, bool large, hipStream_t s);  // many rows
 hipError_t launch_norm(const NormArgs& a, hipStream_t s);
 // rows as for the other quantisers
 hipError_t launch_quant_mxfp4(const uint16_t* X, uint8_t* Q, uint8_t* S, int M, int K, int num_cus,

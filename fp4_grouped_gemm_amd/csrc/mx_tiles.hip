@@ -1,0 +1,718 @@
+// MXFP4 products of many rows (prompts): C = A B^T for rows routed to experts,
+// or silu(A Bg^T) * (A Bu^T) for the gated ones, BF16 or MXFP4 out.
+//
+// A work tile is a window of BM rows and BN rows of B (columns of C, or for
+// gated products the gate and up rows of BN / 2 columns).  A window may hold
+// rows of several experts: the workgroup finds them in m_indices on the device
+// and runs one pass of the K loop for each, storing that expert's rows.
+//
+// K steps of 256 values are 128 bytes a row, a whole cache line, staged in LDS
+// by direct loads while the step before is multiplied; 16-byte chunks (32
+// codes, a block) are XOR-swizzled by row so that fragment reads meet no bank
+// conflict.  v_mfma_scale_f32_16x16x128_f8f6f4 takes a lane's 32 codes and their
+// scale code; which 32 of a step lane (r, q) = (l % 16, l / 16) takes is free as
+// long as A and B agree: blocks 2 q and 2 q + 1, for the step's two products,
+// so that a lane's codes and its two scale bytes are each contiguous.  Scale
+// codes are staged for two steps at a time, 16 bytes a row.
+//
+// B's rows are dealt to the tile's LDS rows so that a lane's sums are eight
+// consecutive columns of a row of C (16 bytes of BF16, or a quarter of an
+// MXFP4 block), and so that gate and up of a column are in the same lane.
+#include "mx.h"
+#include "mx_layout.h"
+#include "offsets.h"
+
+#include <algorithm>
+#include <climits>
+
+namespace fgg {
+namespace mx_tiles_detail {
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
+using namespace lds_dma;
+
+template <int BM_, int BN_, int WAVES_M_, int WAVES_N_, bool GATED_>
+struct Cfg {
+  static constexpr int BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
+  static constexpr bool GATED = GATED_;
+  static constexpr int WAVES = WAVES_M * WAVES_N, THREADS = 64 * WAVES;
+  static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;  // rows of A and of B a wave multiplies
+  static constexpr int TM = WM / 16, TN = WN / 16;
+  static constexpr int COLS = GATED ? BN / 2 : BN;            // columns of C a tile holds
+  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;  // of a K step's tiles
+  static constexpr int A_LOADS = BM / 8 / WAVES, B_LOADS = BN / 8 / WAVES;      // 8 rows a load
+  static constexpr int SCALES = (BM + BN) * 16;               // bytes of two steps' scale codes
+  static constexpr int WG_PER_CU = 160 * 1024 / (2 * (A_BYTES + B_BYTES + SCALES) + 4096);
+  static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0, "load split");
+  static_assert(BM + BN == 64 * WAVES && BM % 64 == 0 && COLS % 64 == 0, "a wave stages 64 rows' scale codes");
+  static_assert(WAVES == 4 || WAVES == 8, "what of a load's place depends on its wave");
+  static_assert(WM == 64 && BM <= 512 && WN % 64 == 0 && TM <= 2 * TN - 4, "tile shape");
+};
+
+// This lane's number, found anew: nothing that is computed from it can be kept
+// in registers from one call to the next.
+__device__ __forceinline__ int fresh_lane() {
+  int l;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+  return l;
+}
+
+// Two steps of A's tile, then two of B's, then two chunks of scale codes (each
+// of two steps, 16 bytes a row: the window's rows, then B's).  What a wave
+// reads of either operand lies within the 64 KB that a read's constant offset
+// spans, so one register holds the place of all its reads.
+template <class T>
+struct Lds {
+  static constexpr int A = 0, B = 2 * T::A_BYTES, SC = B + 2 * T::B_BYTES, BYTES = SC + 2 * T::SCALES;
+  static_assert(2 * T::A_BYTES <= 65536 && 2 * T::B_BYTES <= 65536, "a read's constant offset");
+};
+
+template <class V>
+__device__ __forceinline__ V lds_read(uint32_t at) {
+  return *reinterpret_cast<__attribute__((address_space(3))) const V*>(at);
+}
+
+template <class T>
+struct Pass {
+  i32x4 ra;  // A, the window's rows
+  // B, the tile's rows of the expert.  Of gated products a load holds gate rows
+  // or up rows, by its wave, or with four waves by its number.
+  static constexpr int HALVES = T::GATED && T::WAVES == 4 ? 2 : 1;
+  i32x4 rb[HALVES];
+  i32x4 rs;               // a_scale or b_scale: the 64 rows whose scale codes this wave stages
+  uint32_t lds;           // address of the stages
+  uint32_t a_off, b_off;  // this lane's part of a load's offset
+  uint32_t far;           // kSkip in lanes whose chunk is in a step's second half
+  uint32_t a_at[2], b_at[2], sa_at, sb_at;  // where this lane reads codes (by half) and scale codes
+  uint32_t sc_next;       // the scale codes' buffer that is filled, SCALES or 0
+  uint32_t Kp, Ks;
+  int K128;               // K / 128
+  uint64_t a_groups;      // 8-row groups of the window with a row of this pass
+  f32x4 acc[T::TM][T::TN];
+
+  // Lane l of a load fills chunk l % 8 of its row l / 8 in LDS.
+  __device__ __forceinline__ static int chunk_of(int lane, int wave) {
+    return (lane & 7) ^ off::fp8_swz_key(((wave & 1) << 3) + (lane >> 3));
+  }
+  __device__ __forceinline__ void init(const MxGemmArgs& a, const void* stages, int lane, int wave, int wm, int wn) {
+    Kp = (uint32_t)a.K / 2;
+    Ks = (uint32_t)a.K / 32;
+    K128 = a.K / 128;
+    sc_next = 0;
+    lds = lds_addr(stages);
+    const uint32_t chunk = (uint32_t)chunk_of(lane, wave) * 16u;
+    far = chunk >= 64u ? kSkip : 0u;
+    a_off = (uint32_t)(wave * 8 + (lane >> 3)) * Kp + chunk;
+    b_off = (uint32_t)mx::tile_column(wave, lane >> 3, T::GATED) * Kp + chunk;
+    const int r = lane & 15, q = lane >> 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      a_at[h] = lds + Lds<T>::A + wm * T::WM * 128 + off::fp8_lds_off(r, 2 * q + h);
+      b_at[h] = lds + Lds<T>::B + wn * T::WN * 128 + off::fp8_lds_off(r, 2 * q + h);
+    }
+    sa_at = lds + Lds<T>::SC + (wm * T::WM + r) * 16 + 2 * q;
+    sb_at = lds + Lds<T>::SC + (T::BM + wn * T::WN / (T::GATED ? 2 : 1) + r) * 16 + 2 * q;
+    asm volatile("" : "+v"(a_off), "+v"(b_off), "+v"(far), "+v"(a_at[0]), "+v"(a_at[1]), "+v"(b_at[0]), "+v"(b_at[1]), "+v"(sa_at),
+                 "+v"(sb_at));
+  }
+
+  // Load s of step k into the stage of parity P.  Every wave issues the same
+  // number of loads at every step: those of row groups without a row of the
+  // pass, and of steps past the last, go past the buffer's end (zeros, no
+  // memory is read), and so does the second half of the last step of a K that
+  // is an odd multiple of 128.  (The steps are opaque, so that their sums with
+  // the offsets are not kept in registers over the K loop.)
+  __device__ __forceinline__ i32x4 until_end(i32x4 r, int k) const {
+    r[2] = 2 * k < K128 ? r[2] : 0;
+    return r;
+  }
+  __device__ __forceinline__ uint32_t half_only(int k) const { return 2 * k + 1 == K128 ? far : 0u; }
+  template <int P>
+  __device__ __forceinline__ void load_a(int s, int k, int wave) const {
+    const int b = s * T::WAVES + wave;
+    uint32_t step = (a_groups >> b) & 1 ? (uint32_t)(s * T::WAVES * 8) * Kp : kSkip;
+    asm volatile("" : "+s"(step));
+    dma16(until_end(ra, k), lds + Lds<T>::A + P * T::A_BYTES + b * 1024, (a_off + step) | half_only(k), (uint32_t)k * 128u);
+  }
+  template <int P>
+  __device__ __forceinline__ void load_b(int s, int k, int wave) const {
+    uint32_t step = (uint32_t)mx::tile_step(s, T::WAVES, T::GATED) * Kp;
+    asm volatile("" : "+s"(step));
+    dma16(until_end(rb[HALVES > 1 ? mx::tile_half(s * T::WAVES, true) : 0], k),
+          lds + Lds<T>::B + P * T::B_BYTES + (s * T::WAVES + wave) * 1024, (b_off + step) | half_only(k), (uint32_t)k * 128u);
+  }
+  // The scale codes of steps 2 c and 2 c + 1 into the buffer that the reads do
+  // not go to, 16 bytes a row: a lane a row, or where the row ends among them
+  // four lanes a row, zeros past its end.  Of B a wave's 64 rows lie as their
+  // subtiles do (mx::tile_column), so that the 16 rows of one are read without
+  // a bank conflict.
+  __device__ __forceinline__ void load_scales(int c, int wave) const {
+    const int lane = fresh_lane();
+    const uint32_t to = lds + Lds<T>::SC + sc_next + wave * 1024;
+    const auto row = [&](int p) {
+      const int r = wave * 64 < T::BM ? p : mx::tile_column(p >> 3, p & 7, false);
+      return __umul24((uint32_t)r, Ks);
+    };
+    if (4 * c + 4 <= K128) {
+      dma16(rs, to, row(lane), (uint32_t)c * 16u);
+    } else {
+      const bool past = 4 * c + (lane & 3) >= K128;
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        dma4(rs, to + s * 256, past ? kSkip : row(s * 16 + (lane >> 2)) + (uint32_t)(lane & 3) * 4u, (uint32_t)c * 16u);
+    }
+  }
+  // The reads go on to the next two steps' scale codes.
+  __device__ __forceinline__ void flip_scales() {
+    const uint32_t by = sc_next ? (uint32_t)T::SCALES : 0u - (uint32_t)T::SCALES;
+    sa_at += by;
+    sb_at += by;
+    sc_next = (uint32_t)T::SCALES - sc_next;
+  }
+  __device__ __forceinline__ void set_expert(const MxGemmArgs& a, int e, int row0, int col0, int wave) {
+    const size_t row = (size_t)e * (T::GATED ? 2 : 1) * a.N + col0;
+    const uint32_t rows = (uint32_t)min(T::COLS, a.N - col0);
+#pragma unroll
+    for (int h = 0; h < HALVES; ++h) {
+      const int half = HALVES > 1 ? h : mx::tile_half(wave, T::GATED);
+      rb[h] = rsrc(a.B + (row + (size_t)half * a.N) * Kp, rows * Kp);
+    }
+    // scale rows in LDS: the window's, then the tile's columns (gate, then up)
+    const int r = wave * 64, b = r - T::BM, half = b >= T::COLS ? 1 : 0, n = b - half * T::COLS;
+    const uint8_t* from = r < T::BM ? a.a_scale + (size_t)(row0 + r) * Ks
+                                    : a.b_scale + (row + (size_t)half * a.N + n) * Ks;
+    const int left = r < T::BM ? a.M - row0 - r : (int)rows - n;
+    rs = rsrc(from, left <= 0 ? 0u : left < 64 ? (uint32_t)left * Ks : 64u * Ks);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) rs[i] = __builtin_amdgcn_readfirstlane(rs[i]);
+  }
+
+  // Fragments of half h of a step of parity P: lane (r, q) holds the 32 codes
+  // of block 2 q + h of row r.  The scale codes of blocks 2 q and 2 q + 1 come
+  // in bytes 0 and 1.
+  template <int H, int P>
+  __device__ __forceinline__ i32x4 a_codes(int i) const {
+    return lds_read<i32x4>(a_at[H] + P * T::A_BYTES + i * 2048);
+  }
+  template <int H, int P>
+  __device__ __forceinline__ i32x4 b_codes(int j) const {
+    return lds_read<i32x4>(b_at[H] + P * T::B_BYTES + j * 2048);
+  }
+  template <int P>
+  __device__ __forceinline__ int a_scales(int i) const {
+    return lds_read<uint16_t>(sa_at + P * 8 + i * 256);
+  }
+  template <int P>
+  __device__ __forceinline__ int b_scales(int j) const {
+    // (gate columns' rows lie before up columns')
+    const int row = T::GATED ? (j >> 2) * 32 + (j & 1) * 16 + ((j >> 1) & 1) * T::COLS : j * 16;
+    return lds_read<uint16_t>(sb_at + P * 8 + row * 16);
+  }
+};
+
+template <int H>
+__device__ __forceinline__ f32x4 multiply(i32x4 b, int sb, i32x4 a, int sa, f32x4 acc) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4((i32x8){b[0], b[1], b[2], b[3], 0, 0, 0, 0},
+                                                          (i32x8){a[0], a[1], a[2], a[3], 0, 0, 0, 0}, acc, 4, 4, H, sb,
+                                                          H, sa);
+}
+
+// What a step finds read already: A's fragments of its first half, two of B's.
+template <class T>
+struct Ahead {
+  i32x4 a[T::TM], b[2];
+  int sa[T::TM], sb[2];
+};
+
+// Part 0 .. 3 of that, of a step of parity P.
+template <class T, int P>
+__device__ __forceinline__ void read_ahead(Ahead<T>& x, const Pass<T>& ps, int part) {
+#pragma unroll
+  for (int i = 0; i < T::TM; ++i)
+    if (i % 4 == part) {
+      x.a[i] = ps.template a_codes<0, P>(i);
+      x.sa[i] = ps.template a_scales<P>(i);
+    }
+  if (part >= 2) {
+    x.b[part - 2] = ps.template b_codes<0, P>(part - 2);
+    x.sb[part - 2] = ps.template b_scales<P>(part - 2);
+  }
+}
+
+// Stores of a pass a wave issues.
+template <class T>
+constexpr int stores(bool mx) {
+  return T::TM * T::TN / (T::GATED ? 4 : 2) * (mx ? 2 : 1);
+}
+
+// One K step as 2 TN groups of TM products: half g / TN, column subtile g % TN.
+// B's fragments are read two groups before their use and the last ones before
+// group CUT.  A's part of the step's stage is read by group TM and given up at a
+// barrier there (with few groups at CUT too), to be filled with step k, the one
+// after the next (past the pass's last, a step of the next pass); B's part at
+// CUT, where the next step's loads have arrived; the last four groups cover the
+// reads of the next step's first fragments.  So a load has a step or more to
+// arrive; and the loads are issued one a group, between products.  At the first
+// step of a pass the stores of the pass before, issued after the loads that the
+// step waits for, may still be on their way.
+template <class T, int P, bool ACTIVE>
+__device__ __forceinline__ void kstep(Pass<T>& ps, Ahead<T>& x, int k, bool first, bool mx, int wave) {
+  constexpr int G = 2 * T::TN, CUT = G - 4;
+  constexpr bool SPLIT = CUT > T::TM;
+  constexpr int NEWER = SPLIT ? T::A_LOADS : 0;
+  static_assert(!SPLIT || (T::A_LOADS <= CUT - T::TM && T::B_LOADS <= 4), "loads a group");
+  i32x4 b[G], a1[T::TM];
+  int sb[T::TN];
+  b[0] = x.b[0];
+  b[1] = x.b[1];
+  sb[0] = x.sb[0];
+  sb[1] = x.sb[1];
+  int sa[T::TM];
+#pragma unroll
+  for (int i = 0; i < T::TM; ++i) sa[i] = x.sa[i];
+  const auto read_b = [&](int g) {
+    const int j = g % T::TN;
+    if (g < T::TN) {
+      b[g] = ps.template b_codes<0, P>(j);
+      sb[j] = ps.template b_scales<P>(j);
+    } else {
+      b[g] = ps.template b_codes<1, P>(j);
+    }
+  };
+  const auto group = [&](int g) {
+    const int j = g % T::TN;
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i) {
+      if (g < T::TN)
+        ps.acc[i][j] = multiply<0>(b[g], sb[j], x.a[i], sa[i], ps.acc[i][j]);
+      else
+        ps.acc[i][j] = multiply<1>(b[g], sb[j], a1[i], sa[i], ps.acc[i][j]);
+    }
+    // (an empty statement that names the sums: the products stay ahead of the
+    // reads and loads that follow, instead of sinking past them with their
+    // operands)
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i) asm volatile("" : "+v"(ps.acc[i][j]));
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const auto before_cut = [&](int g) {
+    if (!ACTIVE) return;
+    if (g < CUT - 2) {
+      read_b(g + 2);
+    } else {
+      read_b(2 * g - CUT + 4);
+      read_b(2 * g - CUT + 5);
+    }
+    // A's fragments of the second half, one a group
+    if (g < T::TM) a1[g] = ps.template a_codes<1, P>(g);
+    group(g);
+  };
+#pragma unroll
+  for (int g = 0; g < T::TM; ++g) before_cut(g);
+  if constexpr (SPLIT) {
+    lds_barrier();
+#pragma unroll
+    for (int g = T::TM; g < CUT; ++g) {
+      if (g - T::TM < T::A_LOADS) ps.template load_a<P>(g - T::TM, k, wave);
+      before_cut(g);
+    }
+  }
+  if (P == 0 && first) {
+    if (mx)
+      wait_vmem<NEWER + stores<T>(true)>();
+    else
+      wait_vmem<NEWER + stores<T>(false)>();
+  } else {
+    wait_vmem<NEWER>();
+  }
+  lds_barrier();
+  if (P == 1) ps.flip_scales();
+#pragma unroll
+  for (int g = CUT; g < G; ++g) {
+    if constexpr (!SPLIT) {
+#pragma unroll
+      for (int s = 0; s < T::A_LOADS; ++s)
+        if (s % 4 == g - CUT) ps.template load_a<P>(s, k, wave);
+    }
+#pragma unroll
+    for (int s = 0; s < T::B_LOADS; ++s)
+      if (s % 4 == g - CUT) ps.template load_b<P>(s, k, wave);
+    if (ACTIVE) {
+      read_ahead<T, 1 - P>(x, ps, g - CUT);
+      group(g);
+    }
+  }
+  if (P == 0) ps.load_scales(k / 2, wave);
+}
+
+// Lane l's value of lane l ^ 8, in the lanes of `banks` (bit 2, 3: the upper
+// eight of each 16); the others keep `mine`.
+template <int BANKS>
+__device__ __forceinline__ uint32_t from_half(uint32_t mine, uint32_t theirs) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)mine, (int)theirs, 0x128, 0xF, BANKS, false);  // row_ror:8
+}
+
+// The pass's rows of the sums, eight columns a lane and pair of subtiles.  Two
+// pairs' BF16 results change places between the halves of 16 lanes, so that a
+// store covers whole cache lines: eight rows of 64 columns, not 16 of 32.
+// Every lane stores (through a buffer over the tile's rows; what is not to be
+// stored, past its end), so that a wave's stores can be counted.
+template <class T>
+__device__ __forceinline__ void epilogue(const Pass<T>& ps, const MxGemmArgs& a, int row0, int col0, int wm, int wn, int lane,
+                                         uint64_t rows_ok) {
+  constexpr int STEP = T::GATED ? 4 : 2, PAIRS = T::TN / STEP;  // subtiles of 32 columns
+  const int r = lane & 15, q = lane >> 4;
+  const uint32_t rows = (uint32_t)min(T::BM, a.M - row0), N = (uint32_t)a.N;
+  const bool mx = T::GATED && a.c_scale;
+  const auto at = [](void* p, size_t bytes, uint32_t size) {
+    return __builtin_amdgcn_make_buffer_rsrc(static_cast<uint8_t*>(p) + bytes, (short)0, (int)size, 0x00020000);
+  };
+  const __amdgpu_buffer_rsrc_t rc = at(a.C, (size_t)row0 * N * 2 / (mx ? 4 : 1), rows * N * 2 / (mx ? 4 : 1));
+  const __amdgpu_buffer_rsrc_t rcs = at(a.c_scale, (size_t)row0 * N / 32, mx ? rows * N / 32 : 0u);
+  // place of column n of the wave's row rl, or kSkip (below 2^28)
+  const auto place = [&](int rl, uint32_t n) {
+    return ((rows_ok >> rl) & 1) && n < N ? (uint32_t)(wm * T::WM + rl) * N + n : kSkip;
+  };
+  const uint32_t n0 = (uint32_t)(col0 + wn * PAIRS * 32);
+#pragma unroll
+  for (int i = 0; i < T::TM; ++i) {
+    u32x4 out[PAIRS];
+#pragma unroll
+    for (int p = 0; p < PAIRS; ++p) {
+      const int j = p * STEP;
+      float v[8];
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const float x = ps.acc[i][j + t / 4][t % 4];
+        if constexpr (T::GATED)
+          v[t] = mx::gated(x, ps.acc[i][j + 2 + t / 4][t % 4]);
+        else
+          v[t] = x;
+      }
+      if (mx) {
+        uint32_t top = mx::top8(v);
+        top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+        const uint32_t code = mx::scale_code(top);
+        const uint32_t word = code == 255u ? 0u : mx::codes8(v, mx::inverse(code));
+        const uint32_t to = place(i * 16 + r, n0 + p * 32 + 8 * q);
+        __builtin_amdgcn_raw_buffer_store_b32(word, rc, to == kSkip ? kSkip : to / 2, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b8((uint8_t)code, rcs, to == kSkip || q > 0 ? kSkip : to / 32, 0, 0);
+      } else {
+        const uint2 lo = pack_bf16x4(v[0], v[1], v[2], v[3]), hi = pack_bf16x4(v[4], v[5], v[6], v[7]);
+        out[p] = (u32x4){lo.x, lo.y, hi.x, hi.y};
+      }
+    }
+    if (mx) continue;
+    if constexpr (PAIRS % 2 == 0) {
+#pragma unroll
+      for (int p = 0; p < PAIRS; p += 2) {
+        u32x4 low, high;  // rows 0 .. 7 and 8 .. 15 of the 16
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          low[t] = from_half<0xC>(out[p][t], out[p + 1][t]);
+          high[t] = from_half<0x3>(out[p + 1][t], out[p][t]);
+        }
+        const uint32_t n = n0 + p * 32 + (r >> 3) * 32 + 8 * q;
+        const uint32_t t0 = place(i * 16 + (r & 7), n), t1 = place(i * 16 + 8 + (r & 7), n);
+        __builtin_amdgcn_raw_buffer_store_b128(low, rc, t0 == kSkip ? kSkip : t0 * 2, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(high, rc, t1 == kSkip ? kSkip : t1 * 2, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int p = 0; p < PAIRS; ++p) {
+        const uint32_t to = place(i * 16 + r, n0 + p * 32 + 8 * q);
+        __builtin_amdgcn_raw_buffer_store_b128(out[p], rc, to == kSkip ? kSkip : to * 2, 0, 0);
+      }
+    }
+  }
+}
+
+// A pass: the tile's first row and column, the rows of the tile it may take, and
+// the expert (-1: there is none).
+struct Work {
+  int row0, col0, lo, hi, e;
+};
+
+// A workgroup's items.  The tiles of windows with several experts (`heavy` of
+// them, first in the order of plan_tile) take about two passes, the others one:
+// whole rounds of heavy tiles, then one more heavy tile or two light ones a
+// workgroup, then rounds of light ones.  Where the last round would leave half
+// of the workgroups idle, each of its tiles goes to two of them, half of its
+// rows each: with eight waves a half tile takes one wave a SIMD, and little more
+// than half the time.
+struct Items {
+  int heavy, total, groups, me;  // me of `groups` workgroups
+  int rounds, rest, first, lights, halved;
+
+  __device__ __forceinline__ Items(int heavy_, int total_, bool halves)
+      : heavy(heavy_), total(total_), groups((int)gridDim.x), me((int)blockIdx.x) {
+    rounds = heavy / groups;
+    rest = heavy % groups;
+    first = rest ? 2 * (groups - rest) : 0;
+    lights = max(0, total - heavy - first);
+    const int left = lights % groups;
+    halved = halves && 2 * left <= groups ? left : 0;
+  }
+  // Item n: the tile's place in the order and 0, or 1, 2 for its upper or lower
+  // half; a place of -1 past the last.
+  __device__ __forceinline__ int2 operator()(int n) const {
+    if (n < rounds) return make_int2(n * groups + me, 0);
+    n -= rounds;
+    if (rest) {
+      if (me < rest) {
+        if (n == 0) return make_int2(rounds * groups + me, 0);
+        n -= 1;
+      } else {
+        if (n < 2) {
+          const int i = heavy + n * (groups - rest) + (me - rest);
+          return make_int2(i < total ? i : -1, 0);
+        }
+        n -= 2;
+      }
+    }
+    const int i = n * groups + me, whole = lights - halved, i0 = heavy + first;
+    if (i < whole) return make_int2(i0 + i, 0);
+    if (i - whole < halved) return make_int2(i0 + i, 1);
+    if (i - whole < 2 * halved) return make_int2(i0 + i - halved, 2);
+    return make_int2(-1, 0);
+  }
+};
+
+// The K loop of pass w, whose first two steps have arrived, and in its last two
+// steps the first loads of the pass after it, whose operands `next_pass` sets.
+// A wave without a row of the pass loads its part and computes nothing.
+template <class T, bool ACTIVE, class Next>
+__device__ __forceinline__ void k_loop(Pass<T>& ps, Ahead<T>& x, int nks, bool mx, int wave, Next next_pass) {
+  for (int ks = 0; ks < nks; ks += 2) {
+    int k = ks + 2;
+    if (k == nks) {
+      next_pass();
+      k = 0;
+    }
+    kstep<T, 0, ACTIVE>(ps, x, k, ks == 0, mx, wave);
+    kstep<T, 1, ACTIVE>(ps, x, k + 1, false, mx, wave);
+  }
+}
+
+// A workgroup takes tiles gridDim.x apart, and their passes in turn; the loads
+// go on from one pass to the next without a break.
+template <class T>
+__global__ __launch_bounds__(T::THREADS) void mx_tiles_kernel(const MxGemmArgs a, int num_windows, int num_ntiles, int group_w) {
+  __shared__ __attribute__((aligned(1024))) uint8_t stages[Lds<T>::BYTES];
+  __shared__ __attribute__((aligned(256))) int ids[3][T::BM];  // of the tile before, this one, and the next
+  __shared__ uint32_t plan_bits[kPlanWords];
+  __shared__ int plan_heavy;
+
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
+  Pass<T> ps;
+  ps.init(a, stages, fresh_lane(), wave, wm, wn);
+  const int nks = (ps.K128 + 3) / 4 * 2;  // an even number of steps
+  const bool mx = T::GATED && a.c_scale;
+
+  build_plan<T::BM, T::THREADS>(plan_bits, &plan_heavy, a.m_indices, a.M, a.G, num_windows);
+  const int heavy = plan_heavy;
+
+  const Items items(heavy * num_ntiles, num_windows * num_ntiles, T::WAVES == 8);
+  const auto place_of = [&](int2 item) {
+    int window, ntile;
+    plan_tile(plan_bits, heavy, item.x, num_windows, num_ntiles, group_w, window, ntile);
+    Work w{window * T::BM, ntile * T::COLS, 0, T::BM, -1};
+    if (item.y == 1) w.hi = T::BM / 2;
+    if (item.y == 2) w.lo = T::BM / 2;
+    return w;
+  };
+  // The experts of an item's rows, read by direct loads an item ahead.
+  const auto load_ids = [&](int2 item, int buf) {
+    if (!a.m_indices || item.x < 0 || wave * 64 >= T::BM) return;
+    const int row0 = place_of(item).row0;
+    dma4(rsrc(a.m_indices + row0, (uint32_t)min(T::BM, a.M - row0) * 4u), lds_addr(&ids[buf][wave * 64]),
+         (uint32_t)(wave * 64 + fresh_lane()) * 4u, 0);
+  };
+  const auto id_of = [&](int buf, const Work& w, int r) {
+    if (w.row0 + r >= a.M || r < w.lo || r >= w.hi) return -2;  // never stored
+    const int e = a.m_indices ? ids[buf][r] : 0;
+    return e < 0 || e >= a.G ? -1 : e;
+  };
+
+  int item = 0, buf = 0;
+  Work at{0, 0, 0, 0, -1};  // the item, and in it where the last pass was
+  // The next pass: the next expert in the tile's window, in increasing order, or
+  // the first of the next item that has one; e < 0 past the last.  The rows of
+  // no expert of a new item are filled with zeros here, and the next item's
+  // experts asked for.
+  const auto enter = [&]() {
+    const int lane = fresh_lane();
+    at = place_of(items(item));
+    if (!a.m_indices) return;
+    load_ids(items(item + 1), buf == 2 ? 0 : buf + 1);
+    for (int c = wave * 64 + lane; c < T::BM * (T::COLS / 8); c += T::THREADS) {
+      const int r = c / (T::COLS / 8), col = at.col0 + c % (T::COLS / 8) * 8;
+      if (id_of(buf, at, r) != -1 || col >= a.N) continue;
+      const size_t to = (size_t)(at.row0 + r) * a.N + col;
+      if (mx) {
+        *reinterpret_cast<uint32_t*>(a.C + to / 2) = 0u;
+        if (col % 32 == 0) a.c_scale[to / 32] = 0;
+      } else {
+        *reinterpret_cast<uint4*>(a.C + to * 2) = make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  const auto advance = [&]() {
+    const int lane = fresh_lane();
+    for (bool moved = false;;) {
+      int e = INT_MAX;
+#pragma unroll
+      for (int r = 0; r < T::BM; r += 64) {
+        const int v = id_of(buf, at, r + lane);
+        if (v > at.e && v < e) e = v;
+      }
+      e = __builtin_amdgcn_readfirstlane(wave_min(e));
+      if (e != INT_MAX) {
+        at.e = e;
+        return;
+      }
+      at.e = -1;
+      if (items(++item).x < 0) return;
+      buf = buf == 2 ? 0 : buf + 1;
+      if (moved) {  // the ids were asked for just now
+        wait_vmem<0>();
+        __syncthreads();
+      }
+      moved = true;
+      enter();
+    }
+  };
+  // Sets the loads' operands to those of pass n; past the last, to nothing.
+  uint64_t rows_next = 0;  // the wave's rows of that pass
+  const auto operands = [&](const Work& n) {
+    const int lane = fresh_lane();
+    const int none = n.e < 0 ? 1 : 0;
+    uint64_t groups = 0;
+    if (!none) {
+#pragma unroll
+      for (int r = 0; r < T::BM; r += 64) {  // eight rows a bit
+        uint64_t m = __ballot(id_of(buf, n, r + lane) == n.e);
+        if (r == wm * T::WM) rows_next = m;
+        m |= m >> 1;
+        m |= m >> 2;
+        m |= m >> 4;
+        m &= 0x0101010101010101ull;
+        groups |= ((m * 0x0102040810204080ull) >> 56) << (r / 8);
+      }
+    } else {
+      rows_next = 0;
+    }
+    ps.a_groups = groups;
+    const Work z = none ? Work{0, 0, 0, 0, 0} : n;
+    ps.ra = rsrc(a.A + (size_t)z.row0 * ps.Kp, (uint32_t)min(T::BM, a.M - z.row0) * ps.Kp);
+    ps.set_expert(a, z.e, z.row0, z.col0, wave);
+    if (none) {
+      ps.ra[2] = ps.rs[2] = 0;
+#pragma unroll
+      for (int h = 0; h < ps.HALVES; ++h) ps.rb[h][2] = 0;
+    }
+  };
+
+  if (items(0).x < 0) return;
+  load_ids(items(0), 0);
+  wait_vmem<0>();
+  __syncthreads();
+  enter();
+  wait_vmem<0>();
+  __syncthreads();
+  advance();
+  if (at.e < 0) return;
+  operands(at);
+#pragma unroll
+  for (int i = 0; i < T::A_LOADS; ++i) ps.template load_a<0>(i, 0, wave);
+#pragma unroll
+  for (int i = 0; i < T::B_LOADS; ++i) ps.template load_b<0>(i, 0, wave);
+  ps.load_scales(0, wave);
+  ps.sc_next = T::SCALES;
+#pragma unroll
+  for (int i = 0; i < T::A_LOADS; ++i) ps.template load_a<1>(i, 1, wave);
+#pragma unroll
+  for (int i = 0; i < T::B_LOADS; ++i) ps.template load_b<1>(i, 1, wave);
+  wait_vmem<0>();
+  lds_barrier();
+  Ahead<T> x;
+  bool ahead = false;  // x holds the pass's first fragments
+  for (;;) {
+    const Work w = at;
+    const uint64_t rows = rows_next;
+    advance();
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+      for (int j = 0; j < T::TN; ++j) ps.acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    const auto next_pass = [&]() { operands(at); };
+    if (rows != 0) {
+      if (!ahead) {
+#pragma unroll
+        for (int part = 0; part < 4; ++part) read_ahead<T, 0>(x, ps, part);
+      }
+      k_loop<T, true>(ps, x, nks, mx, wave, next_pass);
+      ahead = true;
+    } else {
+      k_loop<T, false>(ps, x, nks, mx, wave, next_pass);
+      ahead = false;
+    }
+    // (opaque here, so that the stores' addresses are not kept over the K loop)
+    int first_row = w.row0, first_col = w.col0;
+    asm volatile("" : "+s"(first_row), "+s"(first_col));
+    epilogue<T>(ps, a, first_row, first_col, wm, wn, fresh_lane(), rows);
+    if (at.e < 0) break;
+  }
+  wait_vmem<0>();  // the loads past the last pass, which write zeros to LDS
+}
+
+template <class T>
+hipError_t launch(const MxGemmArgs& a, hipStream_t s) {
+  const int num_windows = (a.M + T::BM - 1) / T::BM, num_ntiles = (a.N + T::COLS - 1) / T::COLS;
+  const long long total = (long long)num_windows * num_ntiles;
+  if (total > INT_MAX / 2) return hipErrorInvalidValue;
+  const int slots = a.num_cus * T::WG_PER_CU;
+  const int grid = (int)std::min<long long>(T::WAVES == 8 && 2 * total <= slots ? 2 * total : total, slots);
+  hipLaunchKernelGGL(mx_tiles_kernel<T>, dim3((unsigned)grid), dim3(T::THREADS), 0, s, a, num_windows, num_ntiles, 4);
+  return hipGetLastError();
+}
+
+}  // namespace mx_tiles_detail
+
+// Tiles of 256 rows x 256 columns, or of 128 x 128, two workgroups to a CU.
+hipError_t launch_mx_tiles(const MxGemmArgs& a, bool large, hipStream_t s) {
+  using namespace mx_tiles_detail;
+  if (large) return a.gated ? launch<Cfg<256, 256, 4, 2, true>>(a, s) : launch<Cfg<256, 256, 4, 2, false>>(a, s);
+  return a.gated ? launch<Cfg<128, 128, 2, 2, true>>(a, s) : launch<Cfg<128, 128, 2, 2, false>>(a, s);
+}
+
+// Which kernel, by rows an expert has on average, and columns (a gated column
+// counts as two, its gate and its up row).
+//
+// Few rows: the stream of weights.  It passes over them once for every 32 rows of
+// an expert, where a tile costs nearly the same whatever rows it holds, and one
+// more pass for each further expert that it meets.  Measured, stream | 128 x 128
+// tiles, us, at 40, 55 and 70 rows an expert: 8 experts of 8192 columns, 8192 K, 99
+// | 146, 105 | 121 and 142 | 128; 32 of 2048 columns, 7168 K, 95 | 127, 107 | 129 and
+// 137 | 121; 64 of 2048 columns, 1024 K, 37 | 36 at 40 rows.  Of one expert: 28672
+// columns, 4096 K, 18 | 23 at 32 rows and 27 | 24 at 64.  With few columns K is
+// split over waves, which tiles do not do: 4096 columns and K, 9.5 | 16.4 at 64
+// rows, 16 | 18 at 128 and 23 | 18 at 192.
+//
+// Of the tiles the large ones read their operands half as often; they need rows
+// to fill them and enough of them to fill the card.  128 x 128 | 256 x 256, us: 200
+// rows each for 8 experts of 8192 columns, 8192 K, 158 | 178, 300 rows 207 | 181; of
+// one expert, 4096 columns and K, 2048 rows (128 large tiles) 31 | 32, 1536 rows 26 |
+// 31, 3000 rows 41 | 37; 6144 columns, 4096 K, 777 rows 26 | 29; 28672 columns, 4096
+// K, 512 rows 59 | 42.
+hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t s) {
+  const long long cols = (long long)a.N * (a.gated ? 2 : 1);
+  if (a.M <= 48ll * a.G || (a.M <= 128 && cols * a.G <= 8192)) return launch_mx_rows(a, s);
+  const long long large = ((a.M + 255) / 256) * ((cols + 255) / 256);
+  return launch_mx_tiles(a, a.M >= 256ll * a.G && 2 * large >= a.num_cus, s);
+}
+
+}  // namespace fgg
