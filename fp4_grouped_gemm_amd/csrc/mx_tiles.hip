@@ -674,8 +674,7 @@ hipError_t launch(const MxGemmArgs& a, hipStream_t s) {
   const int num_windows = (a.M + T::BM - 1) / T::BM, num_ntiles = (a.N + T::COLS - 1) / T::COLS;
   const long long total = (long long)num_windows * num_ntiles;
   if (total > INT_MAX / 2) return hipErrorInvalidValue;
-  const int slots = a.num_cus * T::WG_PER_CU;
-  const int grid = (int)std::min<long long>(T::WAVES == 8 && 2 * total <= slots ? 2 * total : total, slots);
+  const int grid = (int)std::min<long long>(total, (long long)a.num_cus * T::WG_PER_CU);
   hipLaunchKernelGGL(mx_tiles_kernel<T>, dim3((unsigned)grid), dim3(T::THREADS), 0, s, a, num_windows, num_ntiles, 4);
   return hipGetLastError();
 }
@@ -712,7 +711,7 @@ hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t s) {
   const long long cols = (long long)a.N * (a.gated ? 2 : 1);
   if (a.M <= 48ll * a.G || (a.M <= 128 && cols * a.G <= 8192)) return launch_mx_rows(a, s);
   const long long large = ((a.M + 255) / 256) * ((cols + 255) / 256);
-  return launch_mx_tiles(a, a.M >= 256ll * a.G && 2 * large >= a.num_cus, s);
+  return launch_mx_tiles(a, a.M >= 256ll * a.G && 2 * large > a.num_cus, s);
 }
 
 }  // namespace fgg
