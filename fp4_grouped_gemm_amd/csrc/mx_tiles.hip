@@ -1,10 +1,12 @@
 // MXFP4 products of many rows (prompts): C = A B^T for rows routed to experts,
 // or silu(A Bg^T) * (A Bu^T) for the gated ones, BF16 or MXFP4 out.
 //
-// A work tile is a window of BM rows and BN rows of B (columns of C, or for
-// gated products the gate and up rows of BN / 2 columns).  A window may hold
-// rows of several experts: the workgroup finds them in m_indices on the device
-// and runs one pass of the K loop for each, storing that expert's rows.
+// A work tile is a span of up to BM rows and BN rows of B (columns of C, or for
+// gated products the gate and up rows of BN / 2 columns).  Where the rows come
+// in runs of one expert, each workgroup finds the runs in m_indices and cuts
+// each into spans of its own; else the spans are windows of BM rows, which may
+// hold rows of several experts, and the workgroup runs one pass of the K loop
+// for each of them, storing that expert's rows.
 //
 // K steps of 256 values are 128 bytes a row, a whole cache line, staged in LDS
 // by direct loads while the step before is multiplied; 16-byte chunks (32
@@ -435,44 +437,142 @@ struct Work {
   int row0, col0, lo, hi, e;
 };
 
-// A workgroup's items.  The tiles of windows with several experts (`heavy` of
-// them, first in the order of plan_tile) take about two passes, the others one:
-// whole rounds of heavy tiles, then one more heavy tile or two light ones a
-// workgroup, then rounds of light ones.  Where the last round would leave half
-// of the workgroups idle, each of its tiles goes to two of them, half of its
-// rows each: with eight waves a half tile takes one wave a SIMD, and little more
-// than half the time.
-struct Items {
-  int heavy, total, groups, me;  // me of `groups` workgroups
-  int rounds, rest, first, lights, halved;
+// The spans that the runs of one expert (or of none) are cut into, as row0 << 8 |
+// rows - 1: those of more than BM / 2 rows from the front of the list, the
+// others from its back, both in the runs' order.
+template <class T>
+struct Spans {
+  static constexpr int CAP = T::WG_PER_CU > 1 ? 1024 : 2048;
+  uint32_t list[CAP];
+  int heavy, light;  // how many; light < 0: not in runs
 
-  __device__ __forceinline__ Items(int heavy_, int total_, bool halves)
-      : heavy(heavy_), total(total_), groups((int)gridDim.x), me((int)blockIdx.x) {
-    rounds = heavy / groups;
-    rest = heavy % groups;
+  // All threads call this; `scratch` is the stages.  Ends with a barrier.  More
+  // runs than two for each expert and one are not taken (of rows in the experts'
+  // order, each with padding behind its rows, there are as many): passes are
+  // then at most that many more than full spans.
+  __device__ __forceinline__ void build(uint8_t* scratch, const int32_t* ids, int M, int G) {
+    constexpr int UNROLL = 8;
+    const int words = (M + 63) / 64, lane = fresh_lane(), wave = (int)threadIdx.x >> 6;
+    uint64_t* first = reinterpret_cast<uint64_t*>(scratch);  // a bit a row: does it begin a run?
+    uint32_t* runs = reinterpret_cast<uint32_t*>(first + words);
+    light = -1;
+    if (words * 8 + (CAP + 1) * 4 > Lds<T>::BYTES) {
+      __syncthreads();
+      return;
+    }
+    const auto key = [&](int e) { return e < 0 || e >= G ? -1 : e; };
+    for (int w0 = wave; w0 < words; w0 += T::WAVES * UNROLL) {
+      int e[UNROLL], before[UNROLL];
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int i = (w0 + u * T::WAVES) * 64 + lane;
+        e[u] = i < M ? ids[i] : 0;
+        before[u] = i < M && i > 0 ? ids[i - 1] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < UNROLL; ++u) {
+        const int w = w0 + u * T::WAVES, i = w * 64 + lane;
+        const uint64_t m = __ballot(i < M && (i == 0 || key(e[u]) != key(before[u])));
+        if (lane == 0 && w < words) first[w] = m;
+      }
+    }
+    __syncthreads();
+    if (wave == 0) {
+      const auto prefix = [&](int v) {  // of the lanes before this one
+        int x = v;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+          const int y = __shfl_up(x, d, 64);
+          if (lane >= d) x += y;
+        }
+        return x - v;
+      };
+      const int most = min(2 * G + 1, CAP);
+      int n = 0;
+      for (int w0 = 0; w0 < words && n <= most; w0 += 64) {
+        uint64_t m = w0 + lane < words ? first[w0 + lane] : 0;
+        const int c = __popcll(m), p = prefix(c);
+        for (int at = n + p; m && at < CAP; m &= m - 1, ++at) runs[at] = (uint32_t)((w0 + lane) * 64 + __builtin_ctzll(m));
+        n += __builtin_amdgcn_readlane(p + c, 63);
+      }
+      int full = 0, part = 0;
+      bool fits = n <= most;
+      for (int r0 = 0; r0 < n && fits; r0 += 64) {
+        const int r = r0 + lane;
+        const int from = r < n ? (int)runs[r] : 0, to = r + 1 < n ? (int)runs[r + 1] : r < n ? M : 0;
+        const int left = (to - from) % T::BM;
+        const bool last_heavy = left > T::BM / 2;
+        const int big = (to - from) / T::BM + last_heavy, small = left > 0 && !last_heavy;
+        int at = full + prefix(big);
+        const int back = part + prefix(small);
+        full = __builtin_amdgcn_readlane(at + big, 63);
+        part = __builtin_amdgcn_readlane(back + small, 63);
+        fits = full + part <= CAP;
+        if (!fits) break;
+        for (int i = from; i < to - (small ? left : 0); i += T::BM) list[at++] = (uint32_t)i << 8 | (uint32_t)(min(to - i, T::BM) - 1);
+        if (small) list[CAP - 1 - back] = (uint32_t)(to - left) << 8 | (uint32_t)(left - 1);
+      }
+      if (lane == 0) {
+        heavy = full;
+        light = fits ? part : -1;
+      }
+    }
+    __syncthreads();
+  }
+};
+
+// A workgroup's items.  Heavy tiles (windows with several experts, about two
+// passes; spans of more than half their rows) come first in the order, and are
+// taken to cost two light ones: whole rounds of heavy tiles, then one more heavy
+// tile or two light ones a workgroup, then rounds of light ones.  With eight
+// waves half the rows of a tile take one wave a SIMD, and little more than half
+// the time.  So where the last round would leave half of the workgroups idle,
+// each of its tiles goes to two of them, half of its rows each: of windows the
+// light ones; of spans the heavy ones of the last round, where that is fewer
+// rounds of light ones than going on as above.
+struct Items {
+  Items() = default;
+  int tall, heavy;   // spans or windows, and heavy ones
+  int total, heavies;  // tiles
+  int rounds, rest, first, lights, halved;
+  bool spans, split;  // split: the last heavy tiles are halved
+
+  __device__ __forceinline__ Items(int tall_, int heavy_, int num_ntiles, bool halves, bool spans_)
+      : tall(tall_), heavy(heavy_), total(tall_ * num_ntiles), heavies(heavy_ * num_ntiles), spans(spans_) {
+    const int groups = (int)gridDim.x;
+    rounds = heavies / groups;
+    rest = heavies % groups;
     first = rest ? 2 * (groups - rest) : 0;
-    lights = max(0, total - heavy - first);
+    lights = max(0, total - heavies - first);
     const int left = lights % groups;
-    halved = halves && 2 * left <= groups ? left : 0;
+    halved = halves && !spans && 2 * left <= groups ? left : 0;
+    split = halves && spans && rest &&
+            (2 * rest + total - heavies + groups - 1) / groups < 2 + (lights + groups - 1) / groups;
   }
   // Item n: the tile's place in the order and 0, or 1, 2 for its upper or lower
   // half; a place of -1 past the last.
   __device__ __forceinline__ int2 operator()(int n) const {
+    const int groups = (int)gridDim.x, me = (int)blockIdx.x;
     if (n < rounds) return make_int2(n * groups + me, 0);
     n -= rounds;
+    if (split) {
+      const int i = n * groups + me;
+      if (i < 2 * rest) return make_int2(rounds * groups + (i < rest ? i : i - rest), i < rest ? 1 : 2);
+      return make_int2(heavies + i - 2 * rest < total ? heavies + i - 2 * rest : -1, 0);
+    }
     if (rest) {
       if (me < rest) {
         if (n == 0) return make_int2(rounds * groups + me, 0);
         n -= 1;
       } else {
         if (n < 2) {
-          const int i = heavy + n * (groups - rest) + (me - rest);
+          const int i = heavies + n * (groups - rest) + (me - rest);
           return make_int2(i < total ? i : -1, 0);
         }
         n -= 2;
       }
     }
-    const int i = n * groups + me, whole = lights - halved, i0 = heavy + first;
+    const int i = n * groups + me, whole = lights - halved, i0 = heavies + first;
     if (i < whole) return make_int2(i0 + i, 0);
     if (i - whole < halved) return make_int2(i0 + i, 1);
     if (i - whole < 2 * halved) return make_int2(i0 + i - halved, 2);
@@ -502,8 +602,12 @@ template <class T>
 __global__ __launch_bounds__(T::THREADS) void mx_tiles_kernel(const MxGemmArgs a, int num_windows, int num_ntiles, int group_w) {
   __shared__ __attribute__((aligned(1024))) uint8_t stages[Lds<T>::BYTES];
   __shared__ __attribute__((aligned(256))) int ids[3][T::BM];  // of the tile before, this one, and the next
-  __shared__ uint32_t plan_bits[kPlanWords];
+  __shared__ union {
+    Spans<T> spans;
+    uint32_t windows[kPlanWords];
+  } plan;
   __shared__ int plan_heavy;
+  __shared__ Items items_lds;  // (not in registers over the K loop)
 
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
@@ -512,26 +616,56 @@ __global__ __launch_bounds__(T::THREADS) void mx_tiles_kernel(const MxGemmArgs a
   const int nks = (ps.K128 + 3) / 4 * 2;  // an even number of steps
   const bool mx = T::GATED && a.c_scale;
 
-  build_plan<T::BM, T::THREADS>(plan_bits, &plan_heavy, a.m_indices, a.M, a.G, num_windows);
-  const int heavy = plan_heavy;
+  if (a.m_indices) plan.spans.build(stages, a.m_indices, a.M, a.G);
+  const bool spans = a.m_indices && __builtin_amdgcn_readfirstlane(plan.spans.light) >= 0;
+  if (spans) {
+    if (threadIdx.x == 0)
+      items_lds = Items(plan.spans.heavy + plan.spans.light, plan.spans.heavy, num_ntiles, T::WAVES == 8, true);
+  } else {
+    __syncthreads();
+    build_plan<T::BM, T::THREADS>(plan.windows, &plan_heavy, a.m_indices, a.M, a.G, num_windows);
+    if (threadIdx.x == 0) items_lds = Items(num_windows, plan_heavy, num_ntiles, T::WAVES == 8, false);
+  }
+  __syncthreads();
 
-  const Items items(heavy * num_ntiles, num_windows * num_ntiles, T::WAVES == 8);
-  const auto place_of = [&](int2 item) {
+  // (inline at every call, so that what they change stays in registers)
+  const auto items = [&](int n) __attribute__((always_inline)) {
+    const int2 i = items_lds(n);
+    return make_int2(__builtin_amdgcn_readfirstlane(i.x), __builtin_amdgcn_readfirstlane(i.y));
+  };
+  const auto place_of = [&](int2 item) __attribute__((always_inline)) {
     int window, ntile;
-    plan_tile(plan_bits, heavy, item.x, num_windows, num_ntiles, group_w, window, ntile);
-    Work w{window * T::BM, ntile * T::COLS, 0, T::BM, -1};
-    if (item.y == 1) w.hi = T::BM / 2;
+    Work w{0, 0, 0, T::BM, -1};
+    const int heavy = items_lds.heavy, tall = items_lds.tall;
+    if (items_lds.spans) {
+      const int split = heavy * num_ntiles;
+      if (item.x < split) {
+        map_tile(item.x, split, heavy, num_ntiles, group_w, window, ntile);
+      } else {
+        map_tile(item.x - split, (tall - heavy) * num_ntiles, tall - heavy, num_ntiles, group_w, window, ntile);
+        window = Spans<T>::CAP - 1 - window;
+      }
+      const uint32_t span = plan.spans.list[window];
+      w.row0 = (int)(span >> 8);
+      w.hi = (int)(span & 255u) + 1;
+    } else {
+      plan_tile(plan.windows, heavy, item.x, num_windows, num_ntiles, group_w, window, ntile);
+      w.row0 = window * T::BM;
+    }
+    w.col0 = ntile * T::COLS;
+    if (item.y == 1) w.hi = min(w.hi, T::BM / 2);
     if (item.y == 2) w.lo = T::BM / 2;
-    return w;
+    const auto same = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+    return Work{same(w.row0), same(w.col0), same(w.lo), same(w.hi), -1};
   };
   // The experts of an item's rows, read by direct loads an item ahead.
-  const auto load_ids = [&](int2 item, int buf) {
+  const auto load_ids = [&](int2 item, int buf) __attribute__((always_inline)) {
     if (!a.m_indices || item.x < 0 || wave * 64 >= T::BM) return;
     const int row0 = place_of(item).row0;
     dma4(rsrc(a.m_indices + row0, (uint32_t)min(T::BM, a.M - row0) * 4u), lds_addr(&ids[buf][wave * 64]),
          (uint32_t)(wave * 64 + fresh_lane()) * 4u, 0);
   };
-  const auto id_of = [&](int buf, const Work& w, int r) {
+  const auto id_of = [&](int buf, const Work& w, int r) __attribute__((always_inline)) {
     if (w.row0 + r >= a.M || r < w.lo || r >= w.hi) return -2;  // never stored
     const int e = a.m_indices ? ids[buf][r] : 0;
     return e < 0 || e >= a.G ? -1 : e;
@@ -543,7 +677,7 @@ __global__ __launch_bounds__(T::THREADS) void mx_tiles_kernel(const MxGemmArgs a
   // the first of the next item that has one; e < 0 past the last.  The rows of
   // no expert of a new item are filled with zeros here, and the next item's
   // experts asked for.
-  const auto enter = [&]() {
+  const auto enter = [&]() __attribute__((always_inline)) {
     const int lane = fresh_lane();
     at = place_of(items(item));
     if (!a.m_indices) return;
@@ -560,7 +694,7 @@ __global__ __launch_bounds__(T::THREADS) void mx_tiles_kernel(const MxGemmArgs a
       }
     }
   };
-  const auto advance = [&]() {
+  const auto advance = [&]() __attribute__((always_inline)) {
     const int lane = fresh_lane();
     for (bool moved = false;;) {
       int e = INT_MAX;
@@ -587,7 +721,7 @@ __global__ __launch_bounds__(T::THREADS) void mx_tiles_kernel(const MxGemmArgs a
   };
   // Sets the loads' operands to those of pass n; past the last, to nothing.
   uint64_t rows_next = 0;  // the wave's rows of that pass
-  const auto operands = [&](const Work& n) {
+  const auto operands = [&](const Work& n) __attribute__((always_inline)) {
     const int lane = fresh_lane();
     const int none = n.e < 0 ? 1 : 0;
     uint64_t groups = 0;
@@ -672,7 +806,9 @@ __global__ __launch_bounds__(T::THREADS) void mx_tiles_kernel(const MxGemmArgs a
 template <class T>
 hipError_t launch(const MxGemmArgs& a, hipStream_t s) {
   const int num_windows = (a.M + T::BM - 1) / T::BM, num_ntiles = (a.N + T::COLS - 1) / T::COLS;
-  const long long total = (long long)num_windows * num_ntiles;
+  // (spans may be more than windows, by no more than the runs)
+  const long long runs = a.m_indices ? std::min(2ll * a.G + 1, (long long)a.M) : 0;
+  const long long total = (num_windows + runs) * num_ntiles;
   if (total > INT_MAX / 2) return hipErrorInvalidValue;
   const int grid = (int)std::min<long long>(total, (long long)a.num_cus * T::WG_PER_CU);
   hipLaunchKernelGGL(mx_tiles_kernel<T>, dim3((unsigned)grid), dim3(T::THREADS), 0, s, a, num_windows, num_ntiles, 4);
@@ -692,26 +828,28 @@ hipError_t launch_mx_tiles(const MxGemmArgs& a, bool large, hipStream_t s) {
 // counts as two, its gate and its up row).
 //
 // Few rows: the stream of weights.  It passes over them once for every 32 rows of
-// an expert, where a tile costs nearly the same whatever rows it holds, and one
-// more pass for each further expert that it meets.  Measured, stream | 128 x 128
-// tiles, us, at 40, 55 and 70 rows an expert: 8 experts of 8192 columns, 8192 K, 99
-// | 146, 105 | 121 and 142 | 128; 32 of 2048 columns, 7168 K, 95 | 127, 107 | 129 and
-// 137 | 121; 64 of 2048 columns, 1024 K, 37 | 36 at 40 rows.  Of one expert: 28672
-// columns, 4096 K, 18 | 23 at 32 rows and 27 | 24 at 64.  With few columns K is
-// split over waves, which tiles do not do: 4096 columns and K, 9.5 | 16.4 at 64
+// an expert, where a tile costs nearly the same whatever rows it holds.  Measured
+// at 16, 24, 32 and 40 rows for each of 32 experts of 2048 columns, 7168 K, stream
+// | 128 x 128 tiles, us: 52 | 57, 57 | 59, 62 | 60 and 99 | 61; of 64 experts of 2048
+// columns, 1024 K, 22 | 29, 26 | 29 and 27 | 30; 16 rows on average, but the r-th
+// expert's share as 1 / r: 94 | 62 and 37 | 33.  (Rows in no order, each window
+// holding all experts, are slower on tiles: 99 | 127 at 40 rows.)  Of one expert:
+// 28672 columns, 4096 K, 18 | 23 at 32 rows and 27 | 24 at 64.  With few columns K
+// is split over waves, which tiles do not do: 4096 columns and K, 9.5 | 16 at 64
 // rows, 16 | 18 at 128 and 23 | 18 at 192.
 //
 // Of the tiles the large ones read their operands half as often; they need rows
-// to fill them and enough of them to fill the card.  128 x 128 | 256 x 256, us: 200
-// rows each for 8 experts of 8192 columns, 8192 K, 158 | 178, 300 rows 207 | 181; of
-// one expert, 4096 columns and K, 2048 rows (128 large tiles) 31 | 32, 1536 rows 26 |
-// 31, 3000 rows 41 | 37; 6144 columns, 4096 K, 777 rows 26 | 29; 28672 columns, 4096
-// K, 512 rows 59 | 42.
+// to fill them and enough of them to fill the card.  128 x 128 | 256 x 256, us: 125,
+// 150, 200 and 300 rows for each of 8 experts of 8192 columns, 8192 K, 91 | 87, 164 |
+// 93, 121 | 96 and 185 | 169; 125 and 250 rows for each of 64 of 1024 gated columns,
+// 2048 K, 54 | 65 and 89 | 78; of one expert, 4096 columns and K, 2048 rows (128 large
+// tiles) 31 | 32, 3000 rows 41 | 37; 6144 columns, 4096 K, 777 rows 26 | 29; 28672
+// columns, 4096 K, 512 rows 59 | 42.
 hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t s) {
   const long long cols = (long long)a.N * (a.gated ? 2 : 1);
-  if (a.M <= 48ll * a.G || (a.M <= 128 && cols * a.G <= 8192)) return launch_mx_rows(a, s);
-  const long long large = ((a.M + 255) / 256) * ((cols + 255) / 256);
-  return launch_mx_tiles(a, a.M >= 256ll * a.G && 2 * large > a.num_cus, s);
+  if (a.M <= std::max(32ll, 24ll * a.G) || (a.M <= 128 && cols * a.G <= 8192)) return launch_mx_rows(a, s);
+  const long long large = std::max((a.M + 255) / 256, a.G) * ((cols + 255) / 256);
+  return launch_mx_tiles(a, a.M > 128ll * a.G && 2 * large > a.num_cus, s);
 }
 
 }  // namespace fgg

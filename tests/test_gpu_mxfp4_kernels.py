@@ -147,3 +147,42 @@ def test_two_streams_at_once():
     for i, (_, want) in enumerate(cases):
         for C in out[i]:
             assert np.array_equal(c_to_f64(C), want)
+
+
+def runs(loads, rng, G):
+    """Rows of (expert, rows) in turn, the experts out of range in several ways."""
+    return np.concatenate([np.full(n, e if 0 <= e < G else rng.choice([-1, G, -7, 2 ** 31 - 1]), np.int32) for e, n in loads])
+
+
+# runs that end at, before and behind half a span and a span; an expert with several runs; more runs than are
+# taken as such; as many heavy spans as fill the card's last round by half, with and without light ones
+RUNS = [(272, 384, 3, [(0, 128), (1, 129), (2, 127), (0, 256), (9, 1), (1, 257), (2, 255), (-1, 300), (0, 1)]),
+        (4112, 256, 3, [(2, 1000), (0, 128), (-1, 129), (1, 897)]), (2064, 128, 2, [(0, 4100), (1, 1)]), (2064, 128, 2, [(-1, 700), (1, 4100)]),
+        (528, 128, 4, [(g % 4, 5 + g) for g in range(60)]), (528, 640, 9, [(g % 9, 40 + 13 * g) for g in range(19)]),
+        (528, 640, 9, [(g % 9, 40 + 13 * g) for g in range(20)]), (4112, 128, 9, [(g, 256 + 60 * (g % 2)) for g in range(9)]),
+        (16, 128, 300, [(g, 100) for g in range(300)]), (48, 128, 600, [(g, 130) for g in range(600)]), (16, 256, 1100, [(g, 30) for g in range(1100)]),
+        (8208, 128, 5, [(g, 513) for g in range(5)]), (1040, 256, 2, [(0, 129), (5, 2000), (1, 130)])]
+
+
+@pytest.mark.parametrize("N,K,G,loads", RUNS)
+def test_runs(N, K, G, loads):
+    rng = np.random.default_rng(N + K + G)
+    ids = runs(loads, rng, G)
+    log(f"runs {len(ids)} {N} {K} {G} {len(loads)}")
+    compare(len(ids), N, K, G, ids, rng)
+
+
+@pytest.mark.parametrize("F,K,G,loads,quantize", [(c[0] - 16, *c[1:], q) for c in RUNS if c[0] > 100 for q in (False, True)])
+def test_runs_gated(F, K, G, loads, quantize):
+    rng = np.random.default_rng(F + K + G)
+    ids = runs(loads, rng, G)
+    A, sA, B, sB, _ = gated_case(len(ids), F, K, G, "one")
+    log(f"runs gated {len(ids)} {F} {K} {G} {len(loads)} {quantize}")
+    out = call_gated(A, sA, B, sB, ids, quantize=quantize)
+    z, halves, S = om.gated(A, B, sA, sB, ids)
+    if quantize:
+        check_mxfp4(host(out[0]), host(out[1]), z, gated_bound(z, halves, S, K))
+        nobody = (ids < 0) | (ids >= G)
+        assert not host(out[0])[nobody].any() and not host(out[1])[nobody].any()
+    else:
+        check_bf16(c_to_f64(out), z, gated_bound(z, halves, S, K))
