@@ -7,15 +7,23 @@
 // come out without a separate dequantisation.
 //
 // With few rows the weights are the traffic, each byte used once, so the kernel
-// is a stream of them: a wave owns 16 or 32 rows of B (of gated products 16 gate
-// rows and the 16 up rows that go with them) over all of K, or a part of K where
-// there are too few columns for all waves; and a ring of two steps of 256 K in
+// is a stream of them: a wave owns 32 rows of B (of gated products 16 gate rows
+// and the 16 up rows that go with them) over all of K, or a part of K where there
+// are too few columns for all waves; and a ring of two or three steps of 256 K in
 // LDS of its own, which it fills by direct loads of whole lines (these stream
-// faster than loads into registers) and reads without waiting for any other
-// wave.  The rows of A that go with an expert are found in scans of m_indices by
-// each wave for itself and come through the same ring, 16 or 32 at a time.  The
-// waves' sums meet in LDS at the end and are added in the waves' order, so
-// results do not depend on timing.
+// faster than loads into registers: 128 rows over 8 experts of 8192 columns and
+// K 55 us against 95) and reads without waiting for any other wave.  The rows of
+// A that go with an expert are found in scans of m_indices by each wave for
+// itself and come through the same ring, 16 or 32 at a time.  The waves' sums meet
+// in LDS at the end and are added in the waves' order, so results do not depend
+// on timing.
+//
+// Measured: 8 experts of 8192 x 8192 (285 MB with scale codes), 8 rows 45 us (6.3
+// TB/s), 128 rows 55 us (5.2 TB/s; a copy on this card reaches 4.6): memory bounds
+// it, and the rows of A that each wave reads for itself.  64 rows of B a wave, with
+// half of that traffic, gained nothing (57 us against 57 at the time) and slowed
+// smaller products; 16 rows nothing for one token (5.9 us against 5.8 at 4096 x
+// 4096, where launches follow each other every 5 us at best).
 #include "mx.h"
 #include "offsets.h"
 
@@ -45,6 +53,13 @@ __device__ __forceinline__ V lds_read(uint32_t at) {
   return *reinterpret_cast<__attribute__((address_space(3))) const V*>(at);
 }
 
+// dma16 of bytes that are not read again: they leave the caches to what is (A
+// and the lines that hold scale codes, 16 bytes a row at a time).
+__device__ __forceinline__ void dma16_once(i32x4 rs, uint32_t lds, uint32_t voff, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds" ::"s"(lds), "v"(voff), "s"(rs), "s"(soff)
+               : "memory", "m0");
+}
+
 // A wave's ring with 16 RB rows of A: three steps of 16 rows, or two of 32, and
 // the scale codes (16 bytes a row) of twice two steps.
 template <class T, int RB>
@@ -72,7 +87,7 @@ struct Stream {
 // Step k into its slot: every step issues the same loads, those past the
 // last step of nothing (zeros, no memory is read), as the second half of an odd
 // multiple of 128 is.
-template <class T, int RB>
+template <class T, int RB, bool ONCE>
 __device__ __forceinline__ void load_step(const Stream& s, uint32_t slot, int k, int lane) {
   const uint32_t at = (uint32_t)k * 128u;
   const bool there = 2 * k < s.K128;
@@ -84,7 +99,11 @@ __device__ __forceinline__ void load_step(const Stream& s, uint32_t slot, int k,
     r[2] = there ? r[2] : 0;
     const uint32_t row = (uint32_t)((T::GATED ? (i & 1) * 8 : i * 8) + (lane >> 3));
     const uint32_t none = 2 * k + 1 == s.K128 && chunk >= 4 ? kSkip : 0u;
-    dma16(r, slot + i * 1024, (row * s.Kp + (uint32_t)chunk * 16u) | none, at);
+    const uint32_t from = (row * s.Kp + (uint32_t)chunk * 16u) | none;
+    if constexpr (ONCE)
+      dma16_once(r, slot + i * 1024, from, at);
+    else
+      dma16(r, slot + i * 1024, from, at);
   }
   i32x4 r = s.ra;
   r[2] = there ? r[2] : 0;
@@ -156,7 +175,7 @@ __device__ __forceinline__ f32x4 multiply(i32x4 b, int sb, i32x4 a, int sa, f32x
 // same memory channels at once where the rows' length is a power of two (8192
 // columns of 8192 K of each of eight experts: 55 us against 59, and 57 against
 // 66 where one wave takes all of K).
-template <class T, int RB>
+template <class T, int RB, bool ONCE>
 __device__ __forceinline__ void stream(const Stream& s, uint32_t ring, int k0, int n, int turn, int lane,
                                        f32x4 (&acc)[2][F]) {
   using R = Ring<T, RB>;
@@ -169,7 +188,7 @@ __device__ __forceinline__ void stream(const Stream& s, uint32_t ring, int k0, i
   for (int i = 0; i < R::N; ++i) {
     // (second of the scale codes' loads before the last step's, as below)
     if (i == R::N - 1) load_scales<T, RB>(s, ring, 1, step(2), lane);
-    load_step<T, RB>(s, ring + i * R::SLOT, step(i), lane);
+    load_step<T, RB, ONCE>(s, ring + i * R::SLOT, step(i), lane);
   }
   uint32_t slot = ring;
   for (int i = 0; i < n; ++i) {
@@ -184,7 +203,7 @@ __device__ __forceinline__ void stream(const Stream& s, uint32_t ring, int k0, i
     read<T, RB>(f, s, ring, slot, i, step(i), lane);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read, before the slot is filled again
     if (i % 2) load_scales<T, RB>(s, ring, i / 2, step(i + 3), lane);
-    load_step<T, RB>(s, slot, step(i + R::N), lane);
+    load_step<T, RB, ONCE>(s, slot, step(i + R::N), lane);
     slot = slot + R::SLOT == ring + R::N * R::SLOT ? ring : slot + R::SLOT;
 #pragma unroll
     for (int m = 0; m < RB; ++m)
@@ -200,7 +219,7 @@ __device__ __forceinline__ void stream(const Stream& s, uint32_t ring, int k0, i
 
 // Rows c0 .. c0 + 16 RB of the expert's (numbered from `base`): the waves' sums,
 // and from them C.
-template <class T, int RB>
+template <class T, int RB, bool ONCE>
 __device__ __forceinline__ void chunk(const MxGemmArgs& a, Stream& s, uint8_t* lds, const uint16_t* rows, int base, int c0, int count,
                                       int n0, int ksplit, int wave, int lane) {
   const uint32_t ring = lds_addr(lds) + wave * ring_bytes<T>();
@@ -219,7 +238,7 @@ __device__ __forceinline__ void chunk(const MxGemmArgs& a, Stream& s, uint8_t* l
   // this wave's part of K: an even number of steps
   const int pairs = (s.K128 + 3) / 4, per = (pairs + ksplit - 1) / ksplit;
   const int p0 = (wave % ksplit) * per, np = __builtin_amdgcn_readfirstlane(min(per, pairs - p0));
-  if (np > 0) stream<T, RB>(s, ring, 2 * p0, 2 * np, 2 * ((int)((blockIdx.x * 5 + wave) & 0xFFFF) % np), lane, acc);
+  if (np > 0) stream<T, RB, ONCE>(s, ring, 2 * p0, 2 * np, 2 * ((int)((blockIdx.x * 5 + wave) & 0xFFFF) % np), lane, acc);
   f32x4* mine = reinterpret_cast<f32x4*>(lds + wave * ring_bytes<T>()) + lane;
 #pragma unroll
   for (int i = 0; i < RB; ++i)
@@ -347,11 +366,22 @@ __global__ __launch_bounds__(T::THREADS, 2) void mx_rows_kernel(const MxGemmArgs
       }
     }
     const uint16_t* list = a.m_indices ? rows : nullptr;
+    // Weights that are read once are asked for as such: 8 experts of 8192 columns
+    // and K, 1 and 16 rows each, 45 and 55 us against 50 and 58; one row of 28672
+    // columns, 4096 K, 13.8 against 14.5; but 64 rows each, two passes over the
+    // weights, 66 against 57.  Where K is split over four waves the weights are few,
+    // and may be in a cache from an earlier call: 4096 x 4096 5.9 against 5.6.
+    const bool once = count <= 32 && a.M <= kScan && ksplit < 4;
     for (int c0 = 0; c0 < count; c0 += 32) {
-      if (count - c0 > 16)
-        chunk<T, 2>(a, s, lds, list, scan0, c0, count, n0, ksplit, wave, lane);
+      const bool two = count - c0 > 16;
+      if (once && two)
+        chunk<T, 2, true>(a, s, lds, list, scan0, c0, count, n0, ksplit, wave, lane);
+      else if (once)
+        chunk<T, 1, true>(a, s, lds, list, scan0, c0, count, n0, ksplit, wave, lane);
+      else if (two)
+        chunk<T, 2, false>(a, s, lds, list, scan0, c0, count, n0, ksplit, wave, lane);
       else
-        chunk<T, 1>(a, s, lds, list, scan0, c0, count, n0, ksplit, wave, lane);
+        chunk<T, 1, false>(a, s, lds, list, scan0, c0, count, n0, ksplit, wave, lane);
     }
   }
 }

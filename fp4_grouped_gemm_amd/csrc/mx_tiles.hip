@@ -832,11 +832,15 @@ hipError_t launch_mx_tiles(const MxGemmArgs& a, bool large, hipStream_t s) {
 // at 16, 24, 32 and 40 rows for each of 32 experts of 2048 columns, 7168 K, stream
 // | 128 x 128 tiles, us: 52 | 57, 57 | 59, 62 | 60 and 99 | 61; of 64 experts of 2048
 // columns, 1024 K, 22 | 29, 26 | 29 and 27 | 30; 16 rows on average, but the r-th
-// expert's share as 1 / r: 94 | 62 and 37 | 33.  (Rows in no order, each window
-// holding all experts, are slower on tiles: 99 | 127 at 40 rows.)  Of one expert:
-// 28672 columns, 4096 K, 18 | 23 at 32 rows and 27 | 24 at 64.  With few columns K
-// is split over waves, which tiles do not do: 4096 columns and K, 9.5 | 16 at 64
-// rows, 16 | 18 at 128 and 23 | 18 at 192.
+// expert's share as 1 / r: 94 | 62 and 37 | 33.  The rows of a decode batch often
+// come in no order, which is nothing to the stream, but windows then hold all
+// experts; so batches of up to 256 rows go there up to 64 rows an expert.  64 rows
+// for each of 4 experts of 8192 columns, 8192 K, 57 | 53 in runs and 58 | 142 in no
+// order; of 4 of 4096 gated columns, 4096 K, 32 | 32 and 33 | 85; 32 rows for each of
+// 8 of 8192 columns, 8192 K, 65 | 84 and 68 | 267.  Of one expert: 28672 columns,
+// 4096 K, 18 | 23 at 32 rows and 27 | 24 at 64.  With few columns K is split over
+// waves, which tiles do not do: 4096 columns and K, 9.5 | 16 at 64 rows, 16 | 18 at
+// 128 and 23 | 18 at 192.
 //
 // Of the tiles the large ones read their operands half as often; they need rows
 // to fill them and enough of them to fill the card.  128 x 128 | 256 x 256, us: 125,
@@ -847,7 +851,8 @@ hipError_t launch_mx_tiles(const MxGemmArgs& a, bool large, hipStream_t s) {
 // columns, 4096 K, 512 rows 59 | 42.
 hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t s) {
   const long long cols = (long long)a.N * (a.gated ? 2 : 1);
-  if (a.M <= std::max(32ll, 24ll * a.G) || (a.M <= 128 && cols * a.G <= 8192)) return launch_mx_rows(a, s);
+  const bool few = a.M <= std::max(32ll, 24ll * a.G) || (a.M <= 256 && a.G > 1 && a.M <= 64ll * a.G);
+  if (few || (a.M <= 128 && cols * a.G <= 8192)) return launch_mx_rows(a, s);
   const long long large = std::max((a.M + 255) / 256, a.G) * ((cols + 255) / 256);
   return launch_mx_tiles(a, a.M > 128ll * a.G && 2 * large > a.num_cus, s);
 }
