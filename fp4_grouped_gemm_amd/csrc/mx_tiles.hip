@@ -616,15 +616,18 @@ __global__ __launch_bounds__(T::THREADS) void mx_tiles_kernel(const MxGemmArgs a
   const int nks = (ps.K128 + 3) / 4 * 2;  // an even number of steps
   const bool mx = T::GATED && a.c_scale;
 
-  if (a.m_indices) plan.spans.build(stages, a.m_indices, a.M, a.G);
-  const bool spans = a.m_indices && __builtin_amdgcn_readfirstlane(plan.spans.light) >= 0;
-  if (spans) {
-    if (threadIdx.x == 0)
-      items_lds = Items(plan.spans.heavy + plan.spans.light, plan.spans.heavy, num_ntiles, T::WAVES == 8, true);
-  } else {
-    __syncthreads();
-    build_plan<T::BM, T::THREADS>(plan.windows, &plan_heavy, a.m_indices, a.M, a.G, num_windows);
-    if (threadIdx.x == 0) items_lds = Items(num_windows, plan_heavy, num_ntiles, T::WAVES == 8, false);
+  if (a.m_indices) {
+    plan.spans.build(stages, a.m_indices, a.M, a.G);
+    const int light = __builtin_amdgcn_readfirstlane(plan.spans.light), spans = plan.spans.heavy;
+    if (light >= 0) {
+      if (threadIdx.x == 0) items_lds = Items(spans + light, spans, num_ntiles, T::WAVES == 8, true);
+    } else {
+      __syncthreads();
+      build_plan<T::BM, T::THREADS>(plan.windows, &plan_heavy, a.m_indices, a.M, a.G, num_windows);
+      if (threadIdx.x == 0) items_lds = Items(num_windows, plan_heavy, num_ntiles, T::WAVES == 8, false);
+    }
+  } else if (threadIdx.x == 0) {
+    items_lds = Items(num_windows, 0, num_ntiles, T::WAVES == 8, false);
   }
   __syncthreads();
 
@@ -697,13 +700,15 @@ __global__ __launch_bounds__(T::THREADS) void mx_tiles_kernel(const MxGemmArgs a
   const auto advance = [&]() __attribute__((always_inline)) {
     const int lane = fresh_lane();
     for (bool moved = false;;) {
-      int e = INT_MAX;
+      int e = !a.m_indices && at.e < 0 ? 0 : INT_MAX;
+      if (a.m_indices) {
 #pragma unroll
-      for (int r = 0; r < T::BM; r += 64) {
-        const int v = id_of(buf, at, r + lane);
-        if (v > at.e && v < e) e = v;
+        for (int r = 0; r < T::BM; r += 64) {
+          const int v = id_of(buf, at, r + lane);
+          if (v > at.e && v < e) e = v;
+        }
+        e = __builtin_amdgcn_readfirstlane(wave_min(e));
       }
-      e = __builtin_amdgcn_readfirstlane(wave_min(e));
       if (e != INT_MAX) {
         at.e = e;
         return;
@@ -751,12 +756,16 @@ __global__ __launch_bounds__(T::THREADS) void mx_tiles_kernel(const MxGemmArgs a
   };
 
   if (items(0).x < 0) return;
-  load_ids(items(0), 0);
-  wait_vmem<0>();
-  __syncthreads();
+  if (a.m_indices) {
+    load_ids(items(0), 0);
+    wait_vmem<0>();
+    __syncthreads();
+  }
   enter();
-  wait_vmem<0>();
-  __syncthreads();
+  if (a.m_indices) {
+    wait_vmem<0>();
+    __syncthreads();
+  }
   advance();
   if (at.e < 0) return;
   operands(at);
