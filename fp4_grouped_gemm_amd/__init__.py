@@ -1,4 +1,4 @@
-"""Block-scaled FP8 / NVFP4 (grouped) GEMM for AMD MI355X (gfx950).
+"""Block-scaled FP8 / NVFP4 / MXFP4 (grouped) GEMM for AMD MI355X (gfx950).
 
 Thin Python binding of ``libfgg.so`` (C ABI in include/fgg.h).  The functions
 take PyTorch tensors only as device memory and streams: they check dtypes,

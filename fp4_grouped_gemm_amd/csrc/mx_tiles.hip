@@ -20,6 +20,18 @@
 // B's rows are dealt to the tile's LDS rows so that a lane's sums are eight
 // consecutive columns of a row of C (16 bytes of BF16, or a quarter of an
 // MXFP4 block), and so that gate and up of a column are in the same lane.
+//
+// Measured: 2048 rows, 36864 columns, 4608 K 191 us (3.6 PFLOP/s); 4096 rows,
+// columns and K 43 us; 5554 rows of 8 experts, 2048 gated columns, 7168 K 125 us.
+// The matrix instruction alone sustains 7.0 PFLOP/s with random operands (power:
+// the clock falls from 2.4 to 2.0 GHz; its 32 x 32 x 64 form 6.3).  A step of 256 x
+// 256 tiles takes 1.7 to 2.1 us, of which 1.1 are matrix instructions; without its
+// loads 1.2.  Of 128 x 128 tiles, one workgroup a CU: 0.8 us, without what its loads
+// bring 0.6, without the loads 0.43, 0.25 of that matrix instructions: reads and
+// writes of LDS come next, then the latency of the loads.  Built and slower or no
+// faster: 32 x 32 x 64 instructions, 128 x 128 products a wave (spills), three
+// stages of 128 x 256 (79 us against 87 for 55 rows of each of 8 experts, but 24
+// against 19 for 512 rows of 4096 columns and K), steps asked for in L2 ahead.
 #include "mx.h"
 #include "mx_layout.h"
 #include "offsets.h"
