@@ -186,3 +186,45 @@ def test_runs_gated(F, K, G, loads, quantize):
         assert not host(out[0])[nobody].any() and not host(out[1])[nobody].any()
     else:
         check_bf16(c_to_f64(out), z, gated_bound(z, halves, S, K))
+
+
+def test_result_over_an_operand():
+    """A result that would overwrite what other workgroups still read is refused; one beside it is not."""
+    import torch
+    M, N, K = 64, 128, 512
+    rng = np.random.default_rng(5)
+    A, sA = coded((M, K), rng, exact_spread(K))
+    B, sB = coded((N, K), rng, exact_spread(K))
+    room = torch.zeros(2 * M * K, dtype=torch.uint8, device="cuda")
+    a = room[:M * K // 2].view(M, K // 2)
+    a.copy_(dev(A))
+    args = [a, dev(B), dev(sA), dev(sB)]
+    with pytest.raises(ValueError, match="overlap"):
+        fgg.mxfp4_gemm(*args, out=room[M * K // 2 - 16:M * K // 2 - 16 + 2 * M * N].view(torch.bfloat16).view(M, N))
+    out = room[M * K // 2:M * K // 2 + 2 * M * N].view(torch.bfloat16).view(M, N)
+    log("result beside an operand")
+    assert fgg.mxfp4_gemm(*args, out=out) is out
+    assert np.array_equal(c_to_f64(out), bf16(om.gemm(A, B, sA, sB)[0]))
+
+
+@pytest.mark.parametrize("quantize", [None, False, True])
+def test_capacity(quantize):
+    """Every expert's rows at the start of as many places, the rest of no expert, some of them empty or full."""
+    G, places, N, K = 6, 400, 1056, 256
+    rng = np.random.default_rng(8)
+    ids = np.full((G, places), -1, np.int32)
+    for e, n in enumerate((0, 400, 1, 129, 300, 256)):
+        ids[e, :n] = e
+    ids = ids.ravel()
+    log(f"capacity {quantize}")
+    if quantize is None:
+        compare(len(ids), N, K, G, ids, rng)
+        return
+    A, sA, B, sB, _ = gated_case(len(ids), N, K, G, "one")
+    out = call_gated(A, sA, B, sB, ids, quantize=quantize)
+    z, halves, S = om.gated(A, B, sA, sB, ids)
+    if quantize:
+        check_mxfp4(host(out[0]), host(out[1]), z, gated_bound(z, halves, S, K))
+        assert not host(out[0])[ids < 0].any() and not host(out[1])[ids < 0].any()
+    else:
+        check_bf16(c_to_f64(out), z, gated_bound(z, halves, S, K))
