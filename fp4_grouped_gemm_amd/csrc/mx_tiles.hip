@@ -166,7 +166,9 @@ struct Pass {
     const uint32_t to = lds + Lds<T>::SC + sc_next + wave * 1024;
     const auto row = [&](int p) {
       const int r = wave * 64 < T::BM ? p : mx::tile_column(p >> 3, p & 7, false);
-      return __umul24((uint32_t)r, Ks);
+      uint32_t at;  // (Ks in a scalar register: held in a vector one it would be spilled)
+      asm("v_mul_u32_u24 %0, %1, %2" : "=v"(at) : "s"(Ks), "v"(r));
+      return at;
     };
     if (4 * c + 4 <= K128) {
       dma16(rs, to, row(lane), (uint32_t)c * 16u);
@@ -449,8 +451,7 @@ struct Work {
   int row0, col0, lo, hi, e;
 };
 
-// The spans that the runs of one expert (or of none) are cut into, as row0 << 8 |
-// rows - 1: those of more than BM / 2 rows from the front of the list, the
+// The spans that the runs of one expert are cut into, as row0 << 8 | rows - 1: those of more than BM / 2 rows from the front of the list, the
 // others from its back, both in the runs' order.
 template <class T>
 struct Spans {
@@ -465,10 +466,12 @@ struct Spans {
   __device__ __forceinline__ void build(uint8_t* scratch, const int32_t* ids, int M, int G) {
     constexpr int UNROLL = 8;
     const int words = (M + 63) / 64, lane = fresh_lane(), wave = (int)threadIdx.x >> 6;
-    uint64_t* first = reinterpret_cast<uint64_t*>(scratch);  // a bit a row: does it begin a run?
-    uint32_t* runs = reinterpret_cast<uint32_t*>(first + words);
+    // a bit a row: does it begin a run?  Is it of no expert?
+    uint64_t* first = reinterpret_cast<uint64_t*>(scratch);
+    uint64_t* none = first + words;
+    uint32_t* runs = reinterpret_cast<uint32_t*>(none + words);  // first row << 1 | of no expert
     light = -1;
-    if (words * 8 + (CAP + 1) * 4 > Lds<T>::BYTES) {
+    if (words * 16 + CAP * 4 > Lds<T>::BYTES) {
       __syncthreads();
       return;
     }
@@ -485,7 +488,11 @@ struct Spans {
       for (int u = 0; u < UNROLL; ++u) {
         const int w = w0 + u * T::WAVES, i = w * 64 + lane;
         const uint64_t m = __ballot(i < M && (i == 0 || key(e[u]) != key(before[u])));
-        if (lane == 0 && w < words) first[w] = m;
+        const uint64_t z = __ballot(i < M && key(e[u]) < 0);
+        if (lane == 0 && w < words) {
+          first[w] = m;
+          none[w] = z;
+        }
       }
     }
     __syncthreads();
@@ -503,15 +510,20 @@ struct Spans {
       int n = 0;
       for (int w0 = 0; w0 < words && n <= most; w0 += 64) {
         uint64_t m = w0 + lane < words ? first[w0 + lane] : 0;
+        const uint64_t z = m ? none[w0 + lane] : 0;
         const int c = __popcll(m), p = prefix(c);
-        for (int at = n + p; m && at < CAP; m &= m - 1, ++at) runs[at] = (uint32_t)((w0 + lane) * 64 + __builtin_ctzll(m));
+        for (int at = n + p; m && at < CAP; m &= m - 1, ++at) {
+          const int b = __builtin_ctzll(m);
+          runs[at] = (uint32_t)((w0 + lane) * 64 + b) << 1 | (uint32_t)(z >> b & 1);
+        }
         n += __builtin_amdgcn_readlane(p + c, 63);
       }
       int full = 0, part = 0;
       bool fits = n <= most;
       for (int r0 = 0; r0 < n && fits; r0 += 64) {
         const int r = r0 + lane;
-        const int from = r < n ? (int)runs[r] : 0, to = r + 1 < n ? (int)runs[r + 1] : r < n ? M : 0;
+        const uint32_t run = r < n ? runs[r] : 1u;
+        const int from = (int)(run >> 1), to = run & 1 ? from : r + 1 < n ? (int)(runs[r + 1] >> 1) : M;
         const int left = (to - from) % T::BM;
         const bool last_heavy = left > T::BM / 2;
         const int big = (to - from) / T::BM + last_heavy, small = left > 0 && !last_heavy;
@@ -627,12 +639,31 @@ __global__ __launch_bounds__(T::THREADS) void mx_tiles_kernel(const MxGemmArgs a
   ps.init(a, stages, fresh_lane(), wave, wm, wn);
   const int nks = (ps.K128 + 3) / 4 * 2;  // an even number of steps
   const bool mx = T::GATED && a.c_scale;
+  const auto clear = [&](int row, int col) __attribute__((always_inline)) {  // eight columns of a row of no expert
+    const size_t to = (size_t)row * a.N + col;
+    if (mx) {
+      *reinterpret_cast<uint32_t*>(a.C + to / 2) = 0u;
+      if (col % 32 == 0) a.c_scale[to / 32] = 0;
+    } else {
+      *reinterpret_cast<uint4*>(a.C + to * 2) = make_uint4(0, 0, 0, 0);
+    }
+  };
 
   if (a.m_indices) {
+    // (rows gridDim.x apart, whose zeros this workgroup writes if they have no expert)
+    int r = (int)(blockIdx.x + threadIdx.x * gridDim.x), e = r < a.M ? a.m_indices[r] : 0;
     plan.spans.build(stages, a.m_indices, a.M, a.G);
     const int light = __builtin_amdgcn_readfirstlane(plan.spans.light), spans = plan.spans.heavy;
     if (light >= 0) {
       if (threadIdx.x == 0) items_lds = Items(spans + light, spans, num_ntiles, T::WAVES == 8, true);
+      for (;;) {
+        const int lane = fresh_lane(), r0 = __builtin_amdgcn_readfirstlane(r);
+        for (uint64_t none = __ballot(r < a.M && (e < 0 || e >= a.G)); none; none &= none - 1)
+          for (int c = 8 * lane; c < a.N; c += 512) clear(r0 + __builtin_ctzll(none) * (int)gridDim.x, c);
+        r += T::THREADS * (int)gridDim.x;
+        if (__ballot(r < a.M) == 0) break;
+        e = r < a.M ? a.m_indices[r] : 0;
+      }
     } else {
       __syncthreads();
       build_plan<T::BM, T::THREADS>(plan.windows, &plan_heavy, a.m_indices, a.M, a.G, num_windows);
@@ -648,6 +679,7 @@ __global__ __launch_bounds__(T::THREADS) void mx_tiles_kernel(const MxGemmArgs a
     const int2 i = items_lds(n);
     return make_int2(__builtin_amdgcn_readfirstlane(i.x), __builtin_amdgcn_readfirstlane(i.y));
   };
+  const auto in_spans = [&]() __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane((int)items_lds.spans) != 0; };
   const auto place_of = [&](int2 item) __attribute__((always_inline)) {
     int window, ntile;
     Work w{0, 0, 0, T::BM, -1};
@@ -690,30 +722,26 @@ __global__ __launch_bounds__(T::THREADS) void mx_tiles_kernel(const MxGemmArgs a
   Work at{0, 0, 0, 0, -1};  // the item, and in it where the last pass was
   // The next pass: the next expert in the tile's window, in increasing order, or
   // the first of the next item that has one; e < 0 past the last.  The rows of
-  // no expert of a new item are filled with zeros here, and the next item's
+  // no expert of a new window are filled with zeros here, and the next item's
   // experts asked for.
   const auto enter = [&]() __attribute__((always_inline)) {
     const int lane = fresh_lane();
     at = place_of(items(item));
     if (!a.m_indices) return;
     load_ids(items(item + 1), buf == 2 ? 0 : buf + 1);
+    if (in_spans()) return;
     for (int c = wave * 64 + lane; c < T::BM * (T::COLS / 8); c += T::THREADS) {
       const int r = c / (T::COLS / 8), col = at.col0 + c % (T::COLS / 8) * 8;
-      if (id_of(buf, at, r) != -1 || col >= a.N) continue;
-      const size_t to = (size_t)(at.row0 + r) * a.N + col;
-      if (mx) {
-        *reinterpret_cast<uint32_t*>(a.C + to / 2) = 0u;
-        if (col % 32 == 0) a.c_scale[to / 32] = 0;
-      } else {
-        *reinterpret_cast<uint4*>(a.C + to * 2) = make_uint4(0, 0, 0, 0);
-      }
+      if (id_of(buf, at, r) == -1 && col < a.N) clear(at.row0 + r, col);
     }
   };
   const auto advance = [&]() __attribute__((always_inline)) {
     const int lane = fresh_lane();
     for (bool moved = false;;) {
-      int e = !a.m_indices && at.e < 0 ? 0 : INT_MAX;
-      if (a.m_indices) {
+      int e = INT_MAX;
+      if (!a.m_indices || in_spans()) {
+        if (at.e < 0) e = a.m_indices ? __builtin_amdgcn_readfirstlane(ids[buf][at.lo]) : 0;
+      } else {
 #pragma unroll
         for (int r = 0; r < T::BM; r += 64) {
           const int v = id_of(buf, at, r + lane);
