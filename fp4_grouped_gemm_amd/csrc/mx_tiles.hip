@@ -4,9 +4,11 @@
 // A work tile is a span of up to BM rows and BN rows of B (columns of C, or for
 // gated products the gate and up rows of BN / 2 columns).  Where the rows come
 // in runs of one expert, each workgroup finds the runs in m_indices and cuts
-// each into spans of its own; else the spans are windows of BM rows, which may
-// hold rows of several experts, and the workgroup runs one pass of the K loop
-// for each of them, storing that expert's rows.
+// each into spans of its own (rows of no expert are in none: the workgroups share
+// out their zeros row by row; 8 experts of 4096 columns and K, 600 rows in 1024
+// places each, 74 us against 100 with tiles of zeros); else the spans are windows
+// of BM rows, which may hold rows of several experts, and the workgroup runs one
+// pass of the K loop for each of them, storing that expert's rows.
 //
 // K steps of 256 values are 128 bytes a row, a whole cache line, staged in LDS
 // by direct loads while the step before is multiplied; 16-byte chunks (32
@@ -22,7 +24,7 @@
 // MXFP4 block), and so that gate and up of a column are in the same lane.
 //
 // Measured: 2048 rows, 36864 columns, 4608 K 191 us (3.6 PFLOP/s); 4096 rows,
-// columns and K 43 us; 5554 rows of 8 experts, 2048 gated columns, 7168 K 125 us.
+// columns and K 43 us; 5554 rows of 8 experts, 2048 gated columns, 7168 K 120 us.
 // The matrix instruction alone sustains 7.0 PFLOP/s with random operands (power:
 // the clock falls from 2.4 to 2.0 GHz; its 32 x 32 x 64 form 6.3).  A step of 256 x
 // 256 tiles takes 1.7 to 2.1 us, of which 1.1 are matrix instructions; without its
