@@ -77,7 +77,6 @@ constexpr int ring_bytes() {
 // A wave's operands: B's rows (of gated products gate and up), and A.
 struct Stream {
   i32x4 rb[2], rsb[2], ra, rsa;
-  uint32_t b_off;         // this lane's part of a load of eight rows of B: row l / 8, chunk l % 8 swizzled
   uint32_t a_off[4];      // of the four loads of A's 32 rows (kSkip: no such row)
   uint32_t as_off;        // scale codes of A's row `lane`
   uint32_t Kp, Ks;
@@ -309,6 +308,7 @@ __global__ __launch_bounds__(T::THREADS, 2) void mx_rows_kernel(const MxGemmArgs
       }
     }
   };
+  int found = 0;
   if (by_row) {
     // The g-th of the experts that have rows (none, -1, among them).
     const int e = lane < a.M ? a.m_indices[lane] : -1, key = e >= 0 && e < a.G ? e : -1;
@@ -322,6 +322,9 @@ __global__ __launch_bounds__(T::THREADS, 2) void mx_rows_kernel(const MxGemmArgs
       for (uint64_t none = __ballot(lane < a.M && key < 0); none && wave == 0; none &= none - 1) clear(__builtin_ctzll(none));
       return;
     }
+    const uint64_t mine = __ballot(lane < a.M && key == g);
+    if (lane < a.M && key == g) rows[__popcll(mine & ((1ull << lane) - 1ull))] = (uint16_t)lane;
+    found = __popcll(mine);
   }
   Stream s;
   s.Kp = (uint32_t)a.K / 2;
@@ -341,7 +344,9 @@ __global__ __launch_bounds__(T::THREADS, 2) void mx_rows_kernel(const MxGemmArgs
     int count = end - scan0;
     s.ra = rsrc(a.A + (size_t)scan0 * s.Kp, (uint32_t)count * s.Kp);
     s.rsa = rsrc(a.a_scale + (size_t)scan0 * s.Ks, (uint32_t)count * s.Ks);
-    if (a.m_indices) {
+    if (by_row) {
+      count = found;
+    } else if (a.m_indices) {
       // Every wave makes the whole list (the same values in the same places),
       // from loads that are all on their way together.
       int e[kScan / 64];
@@ -360,7 +365,7 @@ __global__ __launch_bounds__(T::THREADS, 2) void mx_rows_kernel(const MxGemmArgs
         if (hit) rows[count + __popcll(mask & ((1ull << lane) - 1ull))] = (uint16_t)(m - scan0);
         count += __popcll(mask);
         // (rows of no expert are left to expert 0's workgroups)
-        if (!by_row && g == 0 && wave == 0)
+        if (g == 0 && wave == 0)
           for (uint64_t none = __ballot(m < end && (e[i] < 0 || e[i] >= a.G)); none; none &= none - 1)
             clear(scan0 + i * 64 + __builtin_ctzll(none));
       }
@@ -390,7 +395,7 @@ template <class T>
 hipError_t launch(const MxGemmArgs& a, int ksplit, hipStream_t s) {
   const int cols = T::W / ksplit * T::COLS, nblk = (a.N + cols - 1) / cols;
   // No more experts have rows than there are rows (two rows of eight experts,
-  // 2048 gated columns of 4096 K: 8.8 us against 10.5 with a workgroup for
+  // 2048 gated columns of 4096 K: 8.1 us against 10.5 with a workgroup for
   // every expert; where the workgroups fit the card at once it is the same).
   const bool by_row = a.m_indices && a.M <= 64 && a.M < a.G;
   const long long grid = (long long)nblk * (by_row ? a.M : a.G);

@@ -471,7 +471,9 @@ fgg_status dequantize_mxfp4(const void* Q, const void* scale, void* X, int M, in
  *
  *   A [M, K/2], a_scale [M, K/32];  B [G, N, K/2], b_scale [G, N, K/32]
  *   m_indices [M]  int32 expert id; any value outside [0, G) is padding, whose
- *                  rows of C are zeros.  In any order.
+ *                  rows of C are zeros.  In any order; batches of more than 24
+ *                  rows an expert (64 of up to 256 rows) are fastest where
+ *                  the rows of an expert are runs
  *   C [M, N]       BF16, written in full; must not overlap the operands
  *
  * mxfp4_gated_gemm, grouped_mxfp4_gated_gemm -- the first half of a gated
