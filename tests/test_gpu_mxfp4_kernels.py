@@ -8,7 +8,7 @@ import fp4_grouped_gemm_amd as fgg
 from oracle import mxfp4 as om
 from oracle.formats import bf16_bits_to_float
 from tests.gpu_util import c_bits, c_to_f64, log
-from tests.mxfp4_cases import bf16, check_bf16, check_mxfp4, coded, exact_spread, gated_bound, routed
+from tests.mxfp4_cases import bf16, check_bf16, check_mxfp4, coded, exact_spread, gated_bound, routed, sum_bound
 from tests.test_gpu_mxfp4 import call_gated, dev, gated_case, host
 
 pytestmark = pytest.mark.gpu
@@ -228,3 +228,37 @@ def test_capacity(quantize):
         assert not host(out[0])[ids < 0].any() and not host(out[1])[ids < 0].any()
     else:
         check_bf16(c_to_f64(out), z, gated_bound(z, halves, S, K))
+
+
+@pytest.mark.parametrize("M,N,K,G", [(2, 32, 1 << 20, 1), (150, 32, 1 << 20, 1), (3, 1 << 19, 128, 1), (140, 1 << 19, 128, 1),
+                                     (40, 16, 128, 1 << 16), (300, 16, 128, 1 << 16)])
+def test_largest_sizes(M, N, K, G):
+    """The largest K, N and G that are taken; sums within their bound where FP32 does not hold them."""
+    rng = np.random.default_rng(M)
+    A, sA = coded((M, K), rng, 0)
+    B, sB = coded((G, N, K), rng, 0)
+    log(f"largest sizes {M} {N} {K} {G}")
+    if G == 1:
+        C = fgg.mxfp4_gemm(dev(A), dev(B[0]), dev(sA), dev(sB[0]))
+        want, S = om.gemm(A, B[0], sA, sB[0])
+    else:
+        ids = rng.integers(-1, G, M).astype(np.int32)
+        ids[-1] = G - 1
+        C = fgg.grouped_mxfp4_gemm(dev(A), dev(B), dev(sA), dev(sB), dev(ids))
+        used = np.unique(ids[ids >= 0])
+        want, S = om.gemm(A, B[used], sA, sB[used], np.where(ids < 0, -1, np.searchsorted(used, ids)))
+    check_bf16(c_to_f64(C), want, sum_bound(S, K))
+
+
+@pytest.mark.parametrize("M,G", [(1 << 24, 2), (700001, 3)])
+def test_most_rows(M, G):
+    """More rows than fit the search for runs."""
+    import torch
+    (A, sA), (B, sB) = random_codes((M, 128), 1), random_codes((G, 16, 128), 1)
+    ids = (torch.arange(M, device="cuda") * G // M).int()
+    ids[M // 3:M // 3 + 1000] = -1
+    log(f"most rows {M}")
+    C = fgg.grouped_mxfp4_gemm(A, B, sA, sB, ids)
+    assert not C[M // 3:M // 3 + 1000].any()
+    for rows, e in (([0, 200, M // 4], 0), ([M - 1, M - 300], G - 1)):
+        picked(C, A, B, sA, sB, rows, list(range(16)), e)
