@@ -625,7 +625,8 @@ __device__ __forceinline__ void k_loop(Pass<T>& ps, Ahead<T>& x, int nks, bool m
 // A workgroup takes tiles gridDim.x apart, and their passes in turn; the loads
 // go on from one pass to the next without a break.
 template <class T>
-__global__ __launch_bounds__(T::THREADS) void mx_tiles_kernel(const MxGemmArgs a, int num_windows, int num_ntiles, int group_w) {
+__global__ __launch_bounds__(T::THREADS) void mx_tiles_kernel(const MxGemmArgs a, int num_windows, int num_ntiles) {
+  constexpr int group_w = 4;  // rows of tiles that an XCD's tiles share (1 to 8: all within 3%)
   __shared__ __attribute__((aligned(1024))) uint8_t stages[Lds<T>::BYTES];
   __shared__ __attribute__((aligned(256))) int ids[3][T::BM];  // of the tile before, this one, and the next
   __shared__ union {
@@ -862,7 +863,7 @@ hipError_t launch(const MxGemmArgs& a, hipStream_t s) {
   const long long total = (num_windows + runs) * num_ntiles;
   if (total > INT_MAX / 2) return hipErrorInvalidValue;
   const int grid = (int)std::min<long long>(total, (long long)a.num_cus * T::WG_PER_CU);
-  hipLaunchKernelGGL(mx_tiles_kernel<T>, dim3((unsigned)grid), dim3(T::THREADS), 0, s, a, num_windows, num_ntiles, 4);
+  hipLaunchKernelGGL(mx_tiles_kernel<T>, dim3((unsigned)grid), dim3(T::THREADS), 0, s, a, num_windows, num_ntiles);
   return hipGetLastError();
 }
 
