@@ -262,3 +262,32 @@ def test_most_rows(M, G):
     assert not C[M // 3:M // 3 + 1000].any()
     for rows, e in (([0, 200, M // 4], 0), ([M - 1, M - 300], G - 1)):
         picked(C, A, B, sA, sB, rows, list(range(16)), e)
+
+
+def test_graphs_when_the_routing_changes():
+    """Two captured calls, replayed in turn while the rows' experts change from runs to no order, to one expert,
+    to none: which kernel runs was fixed at capture, where its tiles lie is found at each replay."""
+    import torch
+    rng = np.random.default_rng(21)
+    cases = []
+    for M, N, K, G in ((2600, 2064, 256, 4), (40, 144, 384, 60)):
+        A, sA = coded((M, K), rng, exact_spread(K))
+        B, sB = coded((G, N, K), rng, exact_spread(K))
+        ids = torch.full((M,), -1, dtype=torch.int32, device="cuda")
+        out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+        args = [dev(v) for v in (A, B, sA, sB)]
+        fgg.grouped_mxfp4_gemm(*args, ids, out=out)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            fgg.grouped_mxfp4_gemm(*args, ids, out=out)
+        cases.append((graph, ids, out, args, (A, B, sA, sB), G))
+    for kind in ("runs", "any", "one", "padded", "none", "runs", "any"):
+        for graph, ids, out, _, host_args, G in cases:
+            new = routed(len(ids), G, rng, kind)
+            ids.copy_(dev(new))
+            out.fill_(float("nan"))
+            log(f"graph {len(ids)} {kind}")
+            graph.replay()
+            want, _ = om.gemm(*host_args, new)
+            assert np.array_equal(c_to_f64(out), bf16(want)), kind
