@@ -15,6 +15,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <limits>
 #include <map>
 #include <mutex>
@@ -746,10 +747,40 @@ fgg_status quantize_nvfp4_static_rows(const void* X, const int32_t* rows, void* 
 }
 
 // -------------------------------------------------------------------- MXFP4
+// What a call reads or writes: `rows` rows of `bytes`, `step` bytes apart.
+struct Region {
+  const char* name;
+  const void* at;  // nullptr: nothing
+  unsigned long long bytes, rows = 1, step = 0;
+};
+
+// Results must lie apart from the operands and from each other: workgroups write
+// them while others still read, in no order.
+static fgg_status check_apart(const char* fn, std::initializer_list<Region> results,
+                              std::initializer_list<Region> operands) {
+  // whether a contiguous region meets one of rows
+  const auto meet = [](const Region& c, const Region& r) {
+    if (!c.at || !r.at) return false;
+    const unsigned long long p = (uintptr_t)c.at, q = p + c.bytes, first = (uintptr_t)r.at, end = first + r.bytes;
+    // the first row that ends behind p
+    const unsigned long long i = p < end ? 0 : r.step ? (p - end) / r.step + 1 : r.rows;
+    return i < r.rows && first + i * r.step < q;
+  };
+  for (const Region* c = results.begin(); c != results.end(); ++c) {
+    for (const Region& r : operands)
+      if (meet(*c, r)) return fail(FGG_EINVAL, fn, "%s must not overlap %s", c->name, r.name);
+    for (const Region* d = results.begin(); d != c; ++d)
+      if (meet(*c, *d)) return fail(FGG_EINVAL, fn, "%s must not overlap %s", c->name, d->name);
+  }
+  return FGG_OK;
+}
+
 fgg_status quantize_mxfp4(const void* X, void* Q, void* scale, int M, int K, void* stream) {
   const char* fn = "quantize_mxfp4";
   fgg_status st = check_quant(fn, X, Q, scale, M, K, 1, 32);
   if (st != FGG_OK) return st;
+  const unsigned long long n = (unsigned long long)M * K;
+  if ((st = check_apart(fn, {{"Q", Q, n / 2}, {"scale", scale, n / 32}}, {{"X", X, n * 2}})) != FGG_OK) return st;
   const DeviceFacts* d = current_device(fn, &st);
   if (!d) return st;
   return launched(fn, fgg::launch_quant_mxfp4(static_cast<const uint16_t*>(X), static_cast<uint8_t*>(Q),
@@ -763,6 +794,10 @@ fgg_status quantize_mxfp4_rows(const void* X, const int32_t* rows, void* Q, void
   fgg_status st = check_quant(fn, X, Q, scale, R, K, 1, 32);
   if (st != FGG_OK) return st;
   if ((st = check_rows(fn, rows, R, T, K)) != FGG_OK) return st;
+  const unsigned long long n = (unsigned long long)R * K;
+  st = check_apart(fn, {{"Q", Q, n / 2}, {"scale", scale, n / 32}},
+                   {{"X", X, 2ull * T * K}, {"rows", rows, 4ull * R}});
+  if (st != FGG_OK) return st;
   const DeviceFacts* d = current_device(fn, &st);
   if (!d) return st;
   return launched(fn, fgg::launch_quant_mxfp4(static_cast<const uint16_t*>(X), static_cast<uint8_t*>(Q),
@@ -774,6 +809,8 @@ fgg_status dequantize_mxfp4(const void* Q, const void* scale, void* X, int M, in
   const char* fn = "dequantize_mxfp4";
   fgg_status st = check_quant(fn, X, Q, scale, M, K, 1, 32);
   if (st != FGG_OK) return st;
+  const unsigned long long n = (unsigned long long)M * K;
+  if ((st = check_apart(fn, {{"X", X, n * 2}}, {{"Q", Q, n / 2}, {"scale", scale, n / 32}})) != FGG_OK) return st;
   const DeviceFacts* d = current_device(fn, &st);
   if (!d) return st;
   return launched(fn, fgg::launch_dequant_mxfp4(static_cast<const uint8_t*>(Q),
@@ -806,7 +843,14 @@ static fgg_status mx_gemm(const char* fn, const void* A, const void* B, const vo
   if (!aligned(a_scale, 4) || !aligned(b_scale, 4))
     return fail(FGG_EALIGN, fn, "a_scale and b_scale must be 4-byte aligned");
   if (!aligned(m_indices, 4)) return fail(FGG_EALIGN, fn, "m_indices must be 4-byte aligned");
-  fgg_status st;
+  const unsigned long long m = M, k = K, rows = (unsigned long long)G * N * (gated ? 2 : 1);
+  fgg_status st = check_apart(fn, {{"C", C, m * N * 2 / (c_scale ? 4 : 1)}, {"c_scale", c_scale, m * N / 32}},
+                              {{"A", A, m * k / 2},
+                               {"B", B, rows * k / 2},
+                               {"a_scale", a_scale, m * k / 32},
+                               {"b_scale", b_scale, rows * k / 32},
+                               {"m_indices", m_indices, m * 4}});
+  if (st != FGG_OK) return st;
   const DeviceFacts* d = current_device(fn, &st);
   if (!d) return st;
   const fgg::MxGemmArgs a{static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(B),
@@ -867,6 +911,14 @@ fgg_status residual_norm(const void* x, const void* residual, const void* gate, 
   if ((st = check_vectors(fn, "gate", gate, gate ? strides[2] : 0)) != FGG_OK) return st;
   if (!aligned(post_weight, 16) || !aligned(weight, 16) || !aligned(h, 16) || !aligned(y, 16))
     return fail(FGG_EALIGN, fn, "post_weight, weight, h and y must be 16-byte aligned");
+  const unsigned long long t = T, row = 2ull * H;
+  const auto apart = [&](const char* name, const void* p, long long stride) {
+    return Region{name, p, row, t, 2ull * (unsigned long long)stride};
+  };
+  st = check_apart(fn, {{"h", h, t * row}, {"y", y, t * row / (y_scale ? 4 : 1)}, {"y_scale", y_scale, t * row / 64}},
+                   {apart("x", x, strides[0]), apart("residual", residual, residual ? strides[1] : 0),
+                    apart("gate", gate, gate ? strides[2] : 0), {"post_weight", post_weight, row}, {"weight", weight, row}});
+  if (st != FGG_OK) return st;
   const DeviceFacts* d = current_device(fn, &st);
   if (!d) return st;
   const fgg::NormArgs a{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(residual),

@@ -458,7 +458,8 @@ void fgg_tune_clear(void);
  *
  * Requirements: 1 <= M (R) <= 2^24, 32 <= K <= 2^20 with K % 32 == 0 (else
  * FGG_EINVAL), K % 128 == 0 (else FGG_EUNSUPPORTED); with rows 1 <= T <= 2^24
- * and R * K / 32 < 2^31; X and Q 16-byte, rows 4-byte aligned.
+ * and R * K / 32 < 2^31; X and Q 16-byte, rows 4-byte aligned; what is written
+ * overlaps neither what is read nor itself (else FGG_EINVAL).
  * ------------------------------------------------------------------------ */
 fgg_status quantize_mxfp4(const void* X, void* Q, void* scale, int M, int K, void* stream);
 fgg_status quantize_mxfp4_rows(const void* X, const int32_t* rows, void* Q, void* scale, int R, int T,
@@ -474,7 +475,7 @@ fgg_status dequantize_mxfp4(const void* Q, const void* scale, void* X, int M, in
  *                  rows of C are zeros.  In any order; batches of more than 24
  *                  rows an expert (64 of up to 256 rows) are fastest where
  *                  the rows of an expert are runs
- *   C [M, N]       BF16, written in full; must not overlap the operands
+ *   C [M, N]       BF16, written in full
  *
  * mxfp4_gated_gemm, grouped_mxfp4_gated_gemm -- the first half of a gated
  * feed-forward block, both projections, the activation and the product:
@@ -495,7 +496,8 @@ fgg_status dequantize_mxfp4(const void* Q, const void* scale, void* X, int M, in
  * K % 32 == 0, 1 <= G <= 2^16, F % 32 == 0 for an MXFP4 result (else
  * FGG_EINVAL); N (F) % 16 == 0, K % 128 == 0 and ceil(N / 16) * G < 2^23 (else
  * FGG_EUNSUPPORTED); A, B and C 16-byte, a_scale, b_scale and m_indices 4-byte
- * aligned (else FGG_EALIGN).
+ * aligned (else FGG_EALIGN); C and c_scale overlap neither the operands nor each
+ * other (else FGG_EINVAL).
  */
 fgg_status mxfp4_gemm(const void* A, const void* B, const void* a_scale, const void* b_scale, void* C,
                       int M, int N, int K, void* stream);
@@ -520,8 +522,7 @@ fgg_status grouped_mxfp4_gated_gemm(const void* A, const void* B, const void* a_
  *                      apart (multiples of 8; 0 repeats one row, as a gate
  *                      per channel does); residual NULL: 0, gate NULL: 1
  *   post_weight, weight  BF16 [H]; post_weight NULL: x is not normed
- *   h                  BF16 [T, H], written; must not overlap x, residual or
- *                      gate
+ *   h                  BF16 [T, H], written
  *   y                  BF16 [T, H] if y_scale is NULL, else MXFP4 codes
  *                      [T, H/2] with y_scale [T, H/32], encoded as by
  *                      quantize_mxfp4 from the FP32 results
@@ -529,7 +530,8 @@ fgg_status grouped_mxfp4_gated_gemm(const void* A, const void* B, const void* a_
  * FP32 throughout; y is computed from h before h is rounded.  Squares past
  * FP32's range are infinite.  1 <= T < 2^24, 1 <= H <= 2^20, eps >= 0; H % 8
  * == 0, H % 128 == 0 for an MXFP4 result (else FGG_EUNSUPPORTED, or FGG_EINVAL
- * where that needs whole blocks of 32).
+ * where that needs whole blocks of 32).  h, y and y_scale overlap neither the
+ * operands nor each other (else FGG_EINVAL), so h is not the residual itself.
  */
 fgg_status residual_norm(const void* x, const void* residual, const void* gate,
                          const long long* strides, const void* post_weight, const void* weight,
