@@ -25,9 +25,9 @@
 // smaller products; 16 rows nothing for one token (5.9 us against 5.8 at 4096 x
 // 4096, where launches follow each other every 5 us at best).
 #include "mx.h"
+#include "mx_rule.h"
 #include "offsets.h"
 
-#include <algorithm>
 #include <climits>
 
 namespace fgg {
@@ -406,17 +406,10 @@ hipError_t launch(const MxGemmArgs& a, int ksplit, hipStream_t s) {
 
 }  // namespace mx_rows_detail
 
-// K is split over 4, 2 or 1 of a workgroup's four waves: as much as leaves the
-// card's 2048 waves something to do.  Measured with 4 | 2 | 1, us, one row
-// unless said: 4096 columns of 4096 K 5.6 | 6.4 | 9.0, 8192 of 4096 6.5 | 6.8 |
-// 9.0, 16384 of 4096 10.0 | 9.6 | 12.1, 28672 of 4096 16.5 | 14.2 | 14.1; 192
-// rows over 64 experts, 2048 columns of 1024 K, 38 | 26 | 19.  MXFP4 results
-// need whole blocks of 32 columns in a workgroup, so at most 2 there.
 hipError_t launch_mx_rows(const MxGemmArgs& a, hipStream_t s) {
   using namespace mx_rows_detail;
-  const int cols = a.gated ? Cfg<true>::COLS : Cfg<false>::COLS;
-  const long long waves = (long long)((a.N + cols - 1) / cols) * std::min(a.M, a.G);
-  const int ksplit = waves <= 256 && !a.c_scale ? 4 : waves <= 1024 ? 2 : 1;
+  static_assert(Cfg<true>::COLS == mx::rows_columns(true) && Cfg<false>::COLS == mx::rows_columns(false), "the rule's columns");
+  const int ksplit = mx::rows_ksplit(a.M, a.N, a.G, a.gated, a.c_scale != nullptr);
   return a.gated ? launch<Cfg<true>>(a, ksplit, s) : launch<Cfg<false>>(a, ksplit, s);
 }
 

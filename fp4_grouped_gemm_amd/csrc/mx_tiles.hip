@@ -36,6 +36,7 @@
 // against 19 for 512 rows of 4096 columns and K), steps asked for in L2 ahead.
 #include "mx.h"
 #include "mx_layout.h"
+#include "mx_rule.h"
 #include "offsets.h"
 
 #include <algorithm>
@@ -876,37 +877,9 @@ hipError_t launch_mx_tiles(const MxGemmArgs& a, bool large, hipStream_t s) {
   return a.gated ? launch<Cfg<128, 128, 2, 2, true>>(a, s) : launch<Cfg<128, 128, 2, 2, false>>(a, s);
 }
 
-// Which kernel, by rows an expert has on average, and columns (a gated column
-// counts as two, its gate and its up row).
-//
-// Few rows: the stream of weights.  It passes over them once for every 32 rows of
-// an expert, where a tile costs nearly the same whatever rows it holds.  Measured
-// at 16, 24, 32 and 40 rows for each of 32 experts of 2048 columns, 7168 K, stream
-// | 128 x 128 tiles, us: 52 | 57, 57 | 59, 62 | 60 and 99 | 61; of 64 experts of 2048
-// columns, 1024 K, 22 | 29, 26 | 29 and 27 | 30; 16 rows on average, but the r-th
-// expert's share as 1 / r: 94 | 62 and 37 | 33.  The rows of a decode batch often
-// come in no order, which is nothing to the stream, but windows then hold all
-// experts; so batches of up to 256 rows go there up to 64 rows an expert.  64 rows
-// for each of 4 experts of 8192 columns, 8192 K, 57 | 53 in runs and 58 | 142 in no
-// order; of 4 of 4096 gated columns, 4096 K, 32 | 32 and 33 | 85; 32 rows for each of
-// 8 of 8192 columns, 8192 K, 65 | 84 and 68 | 267.  Of one expert: 28672 columns,
-// 4096 K, 18 | 23 at 32 rows and 27 | 24 at 64.  With few columns K is split over
-// waves, which tiles do not do: 4096 columns and K, 9.5 | 16 at 64 rows, 16 | 18 at
-// 128 and 23 | 18 at 192.
-//
-// Of the tiles the large ones read their operands half as often; they need rows
-// to fill them and enough of them to fill the card.  128 x 128 | 256 x 256, us: 125,
-// 150, 200 and 300 rows for each of 8 experts of 8192 columns, 8192 K, 91 | 87, 164 |
-// 93, 121 | 96 and 185 | 169; 125 and 250 rows for each of 64 of 1024 gated columns,
-// 2048 K, 54 | 65 and 89 | 78; of one expert, 4096 columns and K, 2048 rows (128 large
-// tiles) 31 | 32, 3000 rows 41 | 37; 6144 columns, 4096 K, 777 rows 26 | 29; 28672
-// columns, 4096 K, 512 rows 59 | 42.
 hipError_t launch_mx_gemm(const MxGemmArgs& a, hipStream_t s) {
-  const long long cols = (long long)a.N * (a.gated ? 2 : 1);
-  const bool few = a.M <= std::max(32ll, 24ll * a.G) || (a.M <= 256 && a.G > 1 && a.M <= 64ll * a.G);
-  if (few || (a.M <= 128 && cols * a.G <= 8192)) return launch_mx_rows(a, s);
-  const long long large = std::max((a.M + 255) / 256, a.G) * ((cols + 255) / 256);
-  return launch_mx_tiles(a, a.M > 128ll * a.G && 2 * large > a.num_cus, s);
+  const mx::Kernel k = mx::kernel_for(a.M, a.N, a.G, a.gated, a.num_cus);
+  return k == mx::Kernel::kRows ? launch_mx_rows(a, s) : launch_mx_tiles(a, k == mx::Kernel::kLargeTiles, s);
 }
 
 }  // namespace fgg
