@@ -472,9 +472,13 @@ fgg_status dequantize_mxfp4(const void* Q, const void* scale, void* X, int M, in
  *
  *   A [M, K/2], a_scale [M, K/32];  B [G, N, K/2], b_scale [G, N, K/32]
  *   m_indices [M]  int32 expert id; any value outside [0, G) is padding, whose
- *                  rows of C are zeros.  In any order; batches of more than 24
- *                  rows an expert (64 of up to 256 rows) are fastest where
- *                  the rows of an expert are runs
+ *                  rows of C are zeros.  In any order.  With more than 24 rows
+ *                  an expert (64 in batches of up to 256 rows) rows in no
+ *                  order cost a pass for each expert and window of rows,
+ *                  several times what runs of an expert's rows do; with fewer
+ *                  an expert's weights are streamed once for every 32 of its
+ *                  rows in each 1024 of the batch, so that large batches
+ *                  (4096 rows of 256 experts: twice the time) want runs too
  *   C [M, N]       BF16, written in full
  *
  * mxfp4_gated_gemm, grouped_mxfp4_gated_gemm -- the first half of a gated
