@@ -12,30 +12,7 @@ their contents change.
 """
 from __future__ import annotations
 
-_C = None
-
-
-def _binding():
-    """The compiled module, loaded by the first call: importing the package needs
-    neither torch nor a built library."""
-    global _C
-    import torch  # noqa: F401  (its libraries come first)
-    try:
-        from . import _attention
-    except ImportError as e:
-        raise ImportError("the attention binding is missing or was built for another torch: build it with "
-                          "`python -m fp4_grouped_gemm_amd.build`") from e
-    _C = _attention
-    return _C
-
-
-def _on(stream, q):
-    """A context in which `stream` is the current one, so that memory allocated
-    for the call belongs to the stream that uses it."""
-    import torch
-    if stream.device != q.device:
-        raise ValueError(f"stream is on {stream.device}, expected {q.device}")
-    return torch.cuda.stream(stream)
+from . import compiled
 
 
 def rope_kv_append(q, k, v, cos_sin, positions, page_table, k_cache, v_cache, *, seq_ids=None,
@@ -57,11 +34,11 @@ def rope_kv_append(q, k, v, cos_sin, positions, page_table, k_cache, v_cache, *,
     return_k (rotated queries, rotated keys): what prompt_attention reads.
     See include/fgg.h for the exact definition."""
     if stream is not None:
-        with _on(stream, q):
+        with compiled.on(stream, q):
             return rope_kv_append(q, k, v, cos_sin, positions, page_table, k_cache, v_cache,
                                   seq_ids=seq_ids, interleaved=interleaved, k_scale=k_scale,
                                   v_scale=v_scale, return_k=return_k, out=out)
-    return (_C or _binding()).rope_kv_append(q, k, v, cos_sin, positions, page_table, k_cache, v_cache,
+    return (compiled.C or compiled.load()).rope_kv_append(q, k, v, cos_sin, positions, page_table, k_cache, v_cache,
                                              seq_ids, interleaved, k_scale, v_scale, return_k, out)
 
 
@@ -74,10 +51,10 @@ def paged_decode_attention(q, k_cache, v_cache, page_table, lengths, *, scale=No
     of each sequence (the new one among them); 0 gives zeros.  scale: of the
     scores, D ** -0.5 if None.  Returns bfloat16 [B, Hq, D]."""
     if stream is not None:
-        with _on(stream, q):
+        with compiled.on(stream, q):
             return paged_decode_attention(q, k_cache, v_cache, page_table, lengths, scale=scale,
                                           k_scale=k_scale, v_scale=v_scale, out=out)
-    return (_C or _binding()).paged_decode_attention(q, k_cache, v_cache, page_table, lengths, scale,
+    return (compiled.C or compiled.load()).paged_decode_attention(q, k_cache, v_cache, page_table, lengths, scale,
                                                      k_scale, v_scale, out)
 
 
@@ -91,6 +68,6 @@ def prompt_attention(q, k, v, starts, *, scale=None, out=None, stream=None):
     of those).  scale: of the scores, D ** -0.5 if None.
     Returns bfloat16 [T, Hq, D]."""
     if stream is not None:
-        with _on(stream, q):
+        with compiled.on(stream, q):
             return prompt_attention(q, k, v, starts, scale=scale, out=out)
-    return (_C or _binding()).prompt_attention(q, k, v, starts, scale, out)
+    return (compiled.C or compiled.load()).prompt_attention(q, k, v, starts, scale, out)

@@ -115,7 +115,7 @@ def build(verbose: bool = False) -> str:
     os.replace(tmp, LIB)
     if verbose:
         print("built", LIB)
-        print("built", BINDING) if binding else print("no torch: the attention binding is not built")
+        print("built", BINDING) if binding else print("no torch: the compiled binding is not built")
     return LIB
 
 

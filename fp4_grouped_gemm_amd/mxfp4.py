@@ -14,12 +14,7 @@ can be captured in a HIP graph and replayed after their operands' contents
 """
 from __future__ import annotations
 
-from . import attention as _module
-from .attention import _on
-
-
-def _c():
-    return _module._C or _module._binding()
+from . import compiled
 
 
 def quantize_mxfp4(X, *, rows=None, stream=None):
@@ -29,24 +24,24 @@ def quantize_mxfp4(X, *, rows=None, stream=None):
     rows (int32 [R], optional): the MoE row expansion fused in -- output row r
     quantises X[rows[r]], zeros where rows[r] is outside [0, M)."""
     if stream is not None:
-        with _on(stream, X):
-            return _c().quantize_mxfp4(X, rows)
-    return _c().quantize_mxfp4(X, rows)
+        with compiled.on(stream, X):
+            return (compiled.C or compiled.load()).quantize_mxfp4(X, rows)
+    return (compiled.C or compiled.load()).quantize_mxfp4(X, rows)
 
 
 def dequantize_mxfp4(Q, S, *, stream=None):
     """The values of codes Q [M, K / 2] and scales S [M, K / 32], BF16 [M, K]."""
     if stream is not None:
-        with _on(stream, Q):
-            return _c().dequantize_mxfp4(Q, S)
-    return _c().dequantize_mxfp4(Q, S)
+        with compiled.on(stream, Q):
+            return (compiled.C or compiled.load()).dequantize_mxfp4(Q, S)
+    return (compiled.C or compiled.load()).dequantize_mxfp4(Q, S)
 
 
 def _product(A, B, a_scale, b_scale, m_indices, out, gated, quantize, stream):
     if stream is not None:
-        with _on(stream, A):
-            return _c().mxfp4_product(A, B, a_scale, b_scale, m_indices, out, gated, quantize)
-    return _c().mxfp4_product(A, B, a_scale, b_scale, m_indices, out, gated, quantize)
+        with compiled.on(stream, A):
+            return (compiled.C or compiled.load()).mxfp4_product(A, B, a_scale, b_scale, m_indices, out, gated, quantize)
+    return (compiled.C or compiled.load()).mxfp4_product(A, B, a_scale, b_scale, m_indices, out, gated, quantize)
 
 
 def _routed(m_indices):
@@ -94,6 +89,6 @@ def residual_norm(x, residual, weight, *, post_weight=None, gate=None, scale=1.0
     or None (1).  Returns (y, h): bfloat16 [T, H] both, or with quantize
     ((codes, scales) of y in MXFP4, h)."""
     if stream is not None:
-        with _on(stream, x):
-            return _c().residual_norm(x, residual, weight, post_weight, gate, scale, eps, quantize)
-    return _c().residual_norm(x, residual, weight, post_weight, gate, scale, eps, quantize)
+        with compiled.on(stream, x):
+            return (compiled.C or compiled.load()).residual_norm(x, residual, weight, post_weight, gate, scale, eps, quantize)
+    return (compiled.C or compiled.load()).residual_norm(x, residual, weight, post_weight, gate, scale, eps, quantize)
