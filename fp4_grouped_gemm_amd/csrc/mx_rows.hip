@@ -409,7 +409,7 @@ hipError_t launch(const MxGemmArgs& a, int ksplit, hipStream_t s) {
 hipError_t launch_mx_rows(const MxGemmArgs& a, hipStream_t s) {
   using namespace mx_rows_detail;
   static_assert(Cfg<true>::COLS == mx::rows_columns(true) && Cfg<false>::COLS == mx::rows_columns(false), "the rule's columns");
-  const int ksplit = mx::rows_ksplit(a.M, a.N, a.G, a.gated, a.c_scale != nullptr);
+  const int ksplit = mx::rows_ksplit(a.M, a.N, a.G, a.gated, a.c_scale != nullptr, a.num_cus);
   return a.gated ? launch<Cfg<true>>(a, ksplit, s) : launch<Cfg<false>>(a, ksplit, s);
 }
 

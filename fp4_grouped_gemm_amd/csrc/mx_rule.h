@@ -59,15 +59,16 @@ inline Kernel kernel_for(int M, int N, int G, bool gated, int num_cus) {
 // Columns of C that a wave of the kernel for few rows makes.
 constexpr int rows_columns(bool gated) { return gated ? 16 : 32; }
 
-// K is split over 4, 2 or 1 of a workgroup's four waves: as much as leaves the
-// card's 2048 waves something to do.  Measured with 4 | 2 | 1, us, one row
+// K is split over 4, 2 or 1 of a workgroup's four waves: as much as leaves the card's
+// waves, eight a compute unit, something to do.  Measured with 4 | 2 | 1, us, one row
 // unless said: 4096 columns of 4096 K 5.6 | 6.4 | 9.0, 8192 of 4096 6.5 | 6.8 |
 // 9.0, 16384 of 4096 10.0 | 9.6 | 12.1, 28672 of 4096 16.5 | 14.2 | 14.1; 192
 // rows over 64 experts, 2048 columns of 1024 K, 38 | 26 | 19.  MXFP4 results
-// need whole blocks of 32 columns in a workgroup, so at most 2 there.
-inline int rows_ksplit(int M, int N, int G, bool gated, bool mx_result) {
+// need whole blocks of 32 columns in a workgroup, so at most 2 there.  Both limits
+// are the card's 256 compute units, once and four times.
+inline int rows_ksplit(int M, int N, int G, bool gated, bool mx_result, int num_cus) {
   const long long waves = (long long)((N + rows_columns(gated) - 1) / rows_columns(gated)) * std::min(M, G);
-  return waves <= 256 && !mx_result ? 4 : waves <= 1024 ? 2 : 1;
+  return waves <= num_cus && !mx_result ? 4 : waves <= 4ll * num_cus ? 2 : 1;
 }
 
 }  // namespace mx

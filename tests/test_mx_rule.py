@@ -19,9 +19,9 @@ def kernels(tmp_path_factory):
     subprocess.run(["g++", "-O1", "-std=c++17", "-Wall", "-I", os.path.join(ROOT, "fp4_grouped_gemm_amd", "csrc"),
                     os.path.join(ROOT, "tests", "mx_rule_check.cpp"), "-o", exe], check=True)
 
-    def ask(cases):
+    def ask(cases, cus=256):
         """Kernels of (M, N, G, gated, MXFP4 result)."""
-        lines = "".join("%d %d %d %d %d\n" % tuple(map(int, c)) for c in cases)
+        lines = "".join("%d %d %d %d %d on %d\n" % (*map(int, c), cus) for c in cases)
         return subprocess.run([exe], input=lines, capture_output=True, text=True, timeout=60, check=True).stdout.splitlines()
     return ask
 
@@ -43,3 +43,10 @@ def test_scans_reach_the_stream(kernels):
 def test_repeated_calls_split_k(kernels):
     got = kernels([(M, N, G, 0, 0) for M, N, K, G, ksplit in scans.REPEATED])
     assert got == ["rows %d" % ksplit for M, N, K, G, ksplit in scans.REPEATED] and {k for *_, k in scans.REPEATED} == {1, 2, 4}
+
+
+@pytest.mark.parametrize("cus", [256, 128, 32])
+def test_k_is_split_by_the_card(kernels, cus):
+    """One row: four waves a column block up to one wave a compute unit, two up to four; halves of a card as well."""
+    got = kernels([(1, 32 * w, 1, 0, 0) for w in (cus, cus + 1, 4 * cus, 4 * cus + 1)], cus)
+    assert got == ["rows 4", "rows 2", "rows 2", "rows 1"]
