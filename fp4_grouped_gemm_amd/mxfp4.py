@@ -11,6 +11,9 @@ As the attention operators' these functions check, derive sizes and pass
 pointers on in the compiled module; nothing is read back to the host, so calls
 can be captured in a HIP graph and replayed after their operands' contents
 (the routing among them) change.
+
+A call gives the same bits every time.  A row of a product may have other last
+bits in another batch, where its sums are added in another order.
 """
 from __future__ import annotations
 

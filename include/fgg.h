@@ -454,7 +454,7 @@ void fgg_tune_clear(void);
  * row of zeros.
  *
  * dequantize_mxfp4 -- the values back: X [M, K] = BF16(code * scale), exact but
- * for 4 * 2^127 and 6 * 2^127, which are infinities.
+ * for 2, 3, 4 and 6 times 2^127 (scale code 254), which are infinities.
  *
  * Requirements: 1 <= M (R) <= 2^24, 32 <= K <= 2^20 with K % 32 == 0 (else
  * FGG_EINVAL), K % 128 == 0 (else FGG_EUNSUPPORTED); with rows 1 <= T <= 2^24
@@ -494,7 +494,13 @@ fgg_status dequantize_mxfp4(const void* Q, const void* scale, void* X, int M, in
  *                  its A; rows of padding get codes and scale codes of zero.
  *
  * Sums are FP32, rounded once to the result.  A scale code of 255 makes every
- * result that it reaches NaN.  Rows of padding may hold any bytes.
+ * result that it reaches NaN.  Rows of padding may hold any bytes.  Below a gate
+ * of -88.7, whose exponential is past FP32, silu is -0.
+ *
+ * The same call gives the same bits every time.  A row's sums may be added in
+ * another order in another batch (which kernel, where along K it begins), so
+ * that its last bits may differ there; results whose sums FP32 holds exactly
+ * do not.
  *
  * Requirements: 1 <= M <= 2^24, 16 <= N (F) <= 2^19, 32 <= K <= 2^20 with
  * K % 32 == 0, 1 <= G <= 2^16, F % 32 == 0 for an MXFP4 result (else
@@ -531,11 +537,15 @@ fgg_status grouped_mxfp4_gated_gemm(const void* A, const void* B, const void* a_
  *                      [T, H/2] with y_scale [T, H/32], encoded as by
  *                      quantize_mxfp4 from the FP32 results
  *
- * FP32 throughout; y is computed from h before h is rounded.  Squares past
- * FP32's range are infinite.  1 <= T < 2^24, 1 <= H <= 2^20, eps >= 0; H % 8
- * == 0, H % 128 == 0 for an MXFP4 result (else FGG_EUNSUPPORTED, or FGG_EINVAL
- * where that needs whole blocks of 32).  h, y and y_scale overlap neither the
- * operands nor each other (else FGG_EINVAL), so h is not the residual itself.
+ * FP32 throughout; y is computed from h before h is rounded.  A sum of squares
+ * past FP32's range is infinite and gives a row of y = 0 (from 2^64 / sqrt(H) of
+ * each value on); with eps = 0 a sum below it is zero and gives infinities or
+ * NaN.
+ *
+ * 1 <= T < 2^24, 1 <= H <= 2^20, eps >= 0; H % 8 == 0, H % 128 == 0 for an MXFP4
+ * result (else FGG_EUNSUPPORTED, or FGG_EINVAL where that needs whole blocks of
+ * 32).  h, y and y_scale overlap neither the operands nor each other (else
+ * FGG_EINVAL), so h is not the residual itself.
  */
 fgg_status residual_norm(const void* x, const void* residual, const void* gate,
                          const long long* strides, const void* post_weight, const void* weight,
