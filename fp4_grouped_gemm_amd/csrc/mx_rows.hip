@@ -23,7 +23,7 @@
 // it, and the rows of A that each wave reads for itself.  64 rows of B a wave, with
 // half of that traffic, gained nothing (57 us against 57 at the time) and slowed
 // smaller products; 16 rows nothing for one token (5.9 us against 5.8 at 4096 x
-// 4096, where launches follow each other every 5 us at best).
+// 4096, where calls of the smallest products follow each other every 4 us).
 #include "mx.h"
 #include "mx_rule.h"
 #include "offsets.h"

@@ -12,9 +12,11 @@
 //
 // K steps of 256 values are 128 bytes a row, a whole cache line, staged in LDS
 // by direct loads while the step before is multiplied; 16-byte chunks (32
-// codes, a block) are XOR-swizzled by row so that fragment reads meet no bank
-// conflict.  v_mfma_scale_f32_16x16x128_f8f6f4 takes a lane's 32 codes and their
-// scale code; which 32 of a step lane (r, q) = (l % 16, l / 16) takes is free as
+// codes, a block) are XOR-swizzled by row so that reads of codes meet no bank
+// conflict; the scale codes' reads, two bytes of each of 16 rows 16 bytes apart, meet
+// two cycles of it each (which is all that is counted: 4.0 million for the 2.0
+// million reads of the first case below, 4% of its time).  v_mfma_scale_f32_16x16x128_f8f6f4 takes a lane's 32
+// codes and their scale code; which 32 of a step lane (r, q) = (l % 16, l / 16) takes is free as
 // long as A and B agree: blocks 2 q and 2 q + 1, for the step's two products,
 // so that a lane's codes and its two scale bytes are each contiguous.  Scale
 // codes are staged for two steps at a time, 16 bytes a row.
@@ -24,14 +26,15 @@
 // MXFP4 block), and so that gate and up of a column are in the same lane.
 //
 // Measured: 2048 rows, 36864 columns, 4608 K 191 us (3.6 PFLOP/s); 4096 rows,
-// columns and K 43 us; 5554 rows of 8 experts, 2048 gated columns, 7168 K 120 us.
+// columns and K 43 us; 5554 rows of 8 experts, 2048 gated columns, 7168 K 127 us.
 // The matrix instruction alone sustains 7.0 PFLOP/s with random operands (power:
 // the clock falls from 2.4 to 2.0 GHz; its 32 x 32 x 64 form 6.3).  A step of 256 x
 // 256 tiles takes 1.7 to 2.1 us, of which 1.1 are matrix instructions; without its
 // loads 1.2.  Of 128 x 128 tiles, one workgroup a CU: 0.8 us, without what its loads
 // bring 0.6, without the loads 0.43, 0.25 of that matrix instructions: reads and
 // writes of LDS come next, then the latency of the loads.  Built and slower or no
-// faster: 32 x 32 x 64 instructions, 128 x 128 products a wave (spills), three
+// faster: 32 x 32 x 64 instructions, 128 x 128 products a wave (spills, with the sums
+// in vector registers; in accumulation registers not tried), three
 // stages of 128 x 256 (79 us against 87 for 55 rows of each of 8 experts, but 24
 // against 19 for 512 rows of 4096 columns and K), steps asked for in L2 ahead.
 #include "mx.h"

@@ -320,7 +320,7 @@ __global__ void finalize_kernel(uint32_t* g) {
 // instruction for two values under the scale's reciprocal, a power of two.
 // Bound by memory: 4001 rows of 7168 copied to 10240 rows of experts' runs, 58 MB
 // in and 39 out, 26 us (vector instructions 70% busy); one row of 4096 1.9 us on
-// the GPU, 4.4 a call where calls follow each other.
+// the GPU, 4.4 to 4.9 a call where calls follow each other.
 __global__ __launch_bounds__(kQThreads) void quant_mxfp4_kernel(const uint16_t* __restrict__ X,
                                                                 uint8_t* __restrict__ Q,
                                                                 uint8_t* __restrict__ S,
